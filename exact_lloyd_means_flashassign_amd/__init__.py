@@ -25,6 +25,9 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "fk.h")
 
 METRICS = {"l2": 0, "cosine": 1, "inner_product": 2, "spherical": 3}
 SCORES = {"fp32": 0, "split_bf16": 1}
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+GATES = {"chosen": 0, "all": 1}
 PHASES = ("prep", "assign", "recheck", "sort", "reduce", "finalize", "h2d")
 MAX_K = 65536
 MAX_D = 4096
@@ -46,6 +49,11 @@ class _Profile(ctypes.Structure):
 
 class _FitInfo(ctypes.Structure):
     _fields_ = [("k_used", ctypes.c_int32), ("iterations", ctypes.c_int32), ("last_shift", ctypes.c_double)]
+
+
+class _LinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "ydtype", "bias_dtype", "act", "groups", "share")] + \
+               [(n, ctypes.c_int64) for n in ("M", "N", "K", "ldx", "ldw", "ldr", "ldy", "ldpre")]
 
 
 _lib = None
@@ -79,6 +87,24 @@ def load():
     lib.fk_knn_workspace_size.argtypes = [I64, I32, I64, I32, I32]
     lib.fk_knn_workspace_size.restype = SZ
     lib.fk_knn.argtypes = [P, I64, I32, P, I64, I32, I32, I32, P, P, P, SZ, P]
+    F32 = ctypes.c_float
+    lib.fk_layer_norm.argtypes = [I32, I32, P, I64, I64, I32, P, P, F32, P, I64, P, P, P]
+    lib.fk_layer_norm_backward_workspace_size.argtypes = [I64, I32]
+    lib.fk_layer_norm_backward_workspace_size.restype = SZ
+    lib.fk_layer_norm_backward.argtypes = [I32, I32, P, I64, P, I64, I64, I32, P, P, P, P, I64, P, P, P, SZ, P]
+    lib.fk_route_workspace_size.argtypes = [I64, I32]
+    lib.fk_route_workspace_size.restype = SZ
+    lib.fk_route.argtypes = [I32, P, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]
+    lib.fk_route_backward.argtypes = [I32, P, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, P]
+    lib.fk_linear_workspace_size.argtypes = [ctypes.POINTER(_LinearShape), I32]
+    lib.fk_linear_workspace_size.restype = SZ
+    lib.fk_linear.argtypes = [ctypes.POINTER(_LinearShape), P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.fk_linear_backward.argtypes = [ctypes.POINTER(_LinearShape), P, P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.fk_combine.argtypes = [I32, P, I64, I32, I32, P, P, I64, P, I64, P]
+    lib.fk_combine_backward.argtypes = [I32, P, I64, P, I64, I32, I32, P, P, P, P]
+    for f in ("fk_layer_norm", "fk_layer_norm_backward", "fk_route", "fk_route_backward", "fk_linear",
+              "fk_linear_backward", "fk_combine", "fk_combine_backward"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("fk_assign", "fk_sort_inverse", "fk_update", "fk_lloyd_iter", "fk_lloyd_iter_noalloc", "fk_lloyd_iter_stream",
               "fk_fit", "fk_ivf_build", "fk_knn", "fk_profile_enable", "fk_profile_read"):
         getattr(lib, f).restype = ctypes.c_int
@@ -458,6 +484,315 @@ def fk_knn(Q, DB, k: int, metric="l2", idx=None, dist=None, workspace=None, scor
     _check(load().fk_knn(_ptr(Q), M, d, _ptr(DB), Ndb, k, _metric(metric), _score(score), _ptr(idx), _ptr(dist),
                          ctypes.c_void_p(p), ctypes.c_size_t(n), _stream(Q.device)))
     return idx, dist
+
+
+# ---- the expert block --------------------------------------------------------
+
+
+def _named(table, name, what) -> int:
+    try:
+        return table[name]
+    except KeyError:
+        raise ValueError(f"unknown {what} {name!r}") from None
+
+
+def _typed(t, name, dtypes):
+    """A GPU tensor of one of `dtypes` (any strides)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    return t
+
+
+def _rows(t, name, dtypes, shape=None):
+    """(row stride) of a matrix with contiguous columns."""
+    _typed(t, name, dtypes)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+
+
+def _one_device(*tensors):
+    """The tensors' device, which the call runs on."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors are on different devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+_FLOATS = tuple(DTYPES)
+
+
+def _param(t, name, dtype, shape):
+    """A contiguous parameter of type `dtype` or fp32."""
+    _typed(t, name, (dtype, torch.float32))
+    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def fk_layer_norm(X, weight=None, bias=None, eps: float = 1e-5, Y=None):
+    """Layer norm over the rows of X[rows, d] (fp32, bf16 or fp16; rows may be
+    strided): returns (Y, mean fp32[rows], rstd fp32[rows]).  weight and bias
+    [d] are of X's type or fp32, both of the same."""
+    ldx = _rows(X, "X", _FLOATS)
+    rows, d = X.shape
+    params = [t for t in (weight, bias) if t is not None]
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _param(t, n, X.dtype, (d,))
+    if len({t.dtype for t in params}) > 1:
+        raise ValueError("weight and bias must be of one type")
+    wdt = DTYPES[params[0].dtype if params else X.dtype]
+    if Y is None:
+        Y = torch.empty((rows, d), dtype=X.dtype, device=X.device)
+    ldy = _rows(Y, "Y", (X.dtype,), (rows, d))
+    mean = torch.empty(rows, dtype=torch.float32, device=X.device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+    dev = _one_device(X, weight, bias, Y)
+    with torch.cuda.device(dev):
+        _check(load().fk_layer_norm(DTYPES[X.dtype], wdt, _ptr(X), ldx, rows, d, _ptr(weight), _ptr(bias), float(eps),
+                                    _ptr(Y), ldy, _ptr(mean), _ptr(rstd), _stream(dev)))
+    return Y, mean, rstd
+
+
+def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = True, dX=None, workspace=None):
+    """Gradients of fk_layer_norm: returns (dX, dweight, dbias); dweight and
+    dbias are None without a weight, dbias also with with_bias=False."""
+    ldx = _rows(X, "X", _FLOATS)
+    rows, d = X.shape
+    ldd = _rows(dY, "dY", (X.dtype,), (rows, d))
+    _dev(mean, "mean", torch.float32, (rows,))
+    _dev(rstd, "rstd", torch.float32, (rows,))
+    if dX is None:
+        dX = torch.empty((rows, d), dtype=X.dtype, device=X.device)
+    lddx = _rows(dX, "dX", (X.dtype,), (rows, d))
+    dw = db = None
+    if weight is not None:
+        _param(weight, "weight", X.dtype, (d,))
+        dw = torch.empty_like(weight)
+        db = torch.empty_like(weight) if with_bias else None
+    dev = _one_device(dY, X, mean, rstd, weight, dX)
+    with torch.cuda.device(dev):
+        need = load().fk_layer_norm_backward_workspace_size(rows, d) or 256
+        p, n = _workspace(need, dev, workspace)
+        _check(load().fk_layer_norm_backward(DTYPES[X.dtype], DTYPES[X.dtype if weight is None else weight.dtype],
+                                             _ptr(dY), ldd, _ptr(X), ldx, rows, d, _ptr(mean), _ptr(rstd),
+                                             _ptr(weight), _ptr(dX), lddx, _ptr(dw), _ptr(db), ctypes.c_void_p(p),
+                                             ctypes.c_size_t(n), _stream(dev)))
+    return dX, dw, db
+
+
+def _valid_mask(valid, T):
+    if valid is None:
+        return None
+    _typed(valid, "valid", (torch.bool, torch.uint8))
+    if not valid.is_contiguous() or tuple(valid.shape) != (T,):
+        raise ValueError(f"valid must be contiguous ({T},)")
+    return valid
+
+
+def fk_route(logits, k: int, norm="chosen", valid=None, workspace=None):
+    """Top-k router over logits[T, E]: returns (ids int32[T, k], gates
+    fp32[T, k], counts int32[E], losses fp32[2] = balance and z, live int32[1]).
+    norm: "chosen" (gates sum to 1) or "all" (softmax over every expert).
+    valid: bool or uint8 [T], rows to leave out where it is 0.  A slot without
+    an expert has id E and gate 0."""
+    ldl = _rows(logits, "logits", _FLOATS)
+    T, E = logits.shape
+    k = int(k)
+    _valid_mask(valid, T)
+    dev = _one_device(logits, valid)
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    gates = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    losses = torch.empty(2, dtype=torch.float32, device=dev)
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        need = load().fk_route_workspace_size(T, E) or 256
+        p, n = _workspace(need, dev, workspace)
+        _check(load().fk_route(DTYPES[logits.dtype], _ptr(logits), ldl, T, E, k, _named(GATES, norm, "gate norm"),
+                               _ptr(valid), _ptr(ids), _ptr(gates), _ptr(counts), _ptr(losses), _ptr(live),
+                               ctypes.c_void_p(p), ctypes.c_size_t(n), _stream(dev)))
+    return ids, gates, counts, losses, live
+
+
+def fk_route_backward(logits, ids, counts, live, d_gates=None, d_losses=None, norm="chosen", valid=None):
+    """Gradient of fk_route's gates and losses: returns d_logits [T, E]."""
+    ldl = _rows(logits, "logits", _FLOATS)
+    T, E = logits.shape
+    _dev(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected ({T}, k)")
+    k = ids.shape[1]
+    _dev(counts, "counts", torch.int32, (E,))
+    _dev(live, "live", torch.int32, (1,))
+    if d_gates is not None:
+        _dev(d_gates, "d_gates", torch.float32, (T, k))
+    if d_losses is not None:
+        _dev(d_losses, "d_losses", torch.float32, (2,))
+    _valid_mask(valid, T)
+    dev = _one_device(logits, ids, counts, live, d_gates, d_losses, valid)
+    d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(load().fk_route_backward(DTYPES[logits.dtype], _ptr(logits), ldl, T, E, k,
+                                        _named(GATES, norm, "gate norm"), _ptr(valid), _ptr(ids), _ptr(counts),
+                                        _ptr(live), _ptr(d_gates), _ptr(d_losses), _ptr(d_logits), _stream(dev)))
+    return d_logits
+
+
+def _linear_problem(X, W, act, slots, offsets, share):
+    """The shape struct of a product, its M and the weights' leading shape."""
+    h = _LinearShape()
+    h.ldx = _rows(X, "X", _FLOATS)
+    _typed(W, "W", (X.dtype,))
+    grouped = offsets is not None
+    if W.dim() != (3 if grouped else 2):
+        raise ValueError("W must be [groups, N, K] with offsets, [N, K] without")
+    if grouped and not W.is_contiguous():
+        raise ValueError("grouped W must be contiguous")
+    N, K = W.shape[-2:]
+    if X.shape[1] != K:
+        raise ValueError(f"X has {X.shape[1]} columns, W {K}")
+    h.ldw = K if grouped else _rows(W, "W", (X.dtype,))
+    share = int(share)
+    M = X.shape[0] * max(share, 1)
+    if grouped:
+        _dev(offsets, "offsets", torch.int32)
+        if offsets.dim() != 1 or offsets.shape[0] < W.shape[0] + 1:
+            raise ValueError(f"offsets must hold groups + 1 = {W.shape[0] + 1} entries")
+        if slots is not None:
+            _dev(slots, "slots", torch.int32, (M,))
+    elif slots is not None:
+        raise ValueError("slots need offsets and grouped W")
+    h.dtype = h.ydtype = h.bias_dtype = DTYPES[X.dtype]
+    h.act = _named(ACTS, act, "activation")
+    h.groups = W.shape[0] if grouped else 0
+    h.share = share
+    h.M, h.N, h.K = M, N, K
+    h.ldr = h.ldy = h.ldpre = max(N, 1)
+    return h
+
+
+def fk_linear(X, W, bias=None, act="none", residual=None, slots=None, offsets=None, share: int = 1,
+              with_pre: bool = False, out_dtype=None, Y=None, workspace=None):
+    """Y = act(X W^T + bias) + residual: returns (Y, pre), pre being the
+    pre-activations when with_pre is set (fk_linear_backward takes them), else
+    None.  W is [N, K], or with offsets [groups, N, K]: then slot
+    s = slots[p] of group g (offsets[g] <= p < offsets[g+1]) is row s of Y and
+    takes row s // share of X (X holds M / share rows); offsets may have more
+    entries than groups + 1 (fk_sort_inverse of E + 1 clusters), and the slots
+    past offsets[groups] give zero rows.  Y is of X's type or, with
+    out_dtype=torch.float32, fp32."""
+    h = _linear_problem(X, W, act, slots, offsets, share)
+    shape = (h.M, h.N)
+    if Y is None:
+        Y = torch.empty(shape, dtype=out_dtype or X.dtype, device=X.device)
+    h.ldy = _rows(Y, "Y", (X.dtype, torch.float32), shape)
+    h.ydtype = DTYPES[Y.dtype]
+    if out_dtype is not None and Y.dtype != out_dtype:
+        raise ValueError(f"Y is {Y.dtype}, out_dtype {out_dtype}")
+    if bias is not None:
+        _param(bias, "bias", X.dtype, W.shape[:-1])
+        h.bias_dtype = DTYPES[bias.dtype]
+    if residual is not None:
+        h.ldr = _rows(residual, "residual", (X.dtype,), shape)
+    pre = torch.empty(shape, dtype=X.dtype, device=X.device) if with_pre else None
+    dev = _one_device(X, W, bias, residual, slots, offsets, Y)
+    with torch.cuda.device(dev):
+        need = load().fk_linear_workspace_size(ctypes.byref(h), 0) or 256
+        p, n = _workspace(need, dev, workspace)
+        _check(load().fk_linear(ctypes.byref(h), _ptr(X), _ptr(W), _ptr(bias), _ptr(residual), _ptr(slots),
+                                _ptr(offsets), _ptr(Y), _ptr(pre), ctypes.c_void_p(p), ctypes.c_size_t(n),
+                                _stream(dev)))
+    return Y, pre
+
+
+def fk_linear_backward(dY, X, W, act="none", pre=None, slots=None, offsets=None, share: int = 1,
+                       with_dx: bool = True, with_dw: bool = True, with_bias: bool = True, bias_dtype=None,
+                       workspace=None):
+    """Gradients of fk_linear: returns (dX, dW, dbias), None for those not
+    asked for.  dX has a row for each slot (with share > 1, fk_combine without
+    gates adds the rows that share one of X); dW and dbias have the shapes of W
+    and the bias.  pre: what fk_linear kept (needed unless act is "none")."""
+    h = _linear_problem(X, W, act, slots, offsets, share)
+    shape = (h.M, h.N)
+    h.ldy = _rows(dY, "dY", (X.dtype, torch.float32), shape)
+    h.ydtype = DTYPES[dY.dtype]
+    if pre is not None:
+        h.ldpre = _rows(pre, "pre", (X.dtype,), shape)
+    elif h.act != 0:
+        raise ValueError(f"act {act!r} needs pre")
+    bias_dtype = bias_dtype or X.dtype
+    if bias_dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"bias_dtype must be {X.dtype} or torch.float32")
+    h.bias_dtype = DTYPES[bias_dtype]
+    dev = _one_device(dY, X, W, pre, slots, offsets)
+    dX = torch.empty((h.M, h.K), dtype=X.dtype, device=dev) if with_dx else None
+    dW = torch.empty(W.shape, dtype=X.dtype, device=dev) if with_dw else None
+    db = torch.empty(W.shape[:-1], dtype=bias_dtype, device=dev) if with_bias else None
+    with torch.cuda.device(dev):
+        need = load().fk_linear_workspace_size(ctypes.byref(h), 1) or 256
+        p, n = _workspace(need, dev, workspace)
+        _check(load().fk_linear_backward(ctypes.byref(h), _ptr(dY), _ptr(X), _ptr(W), _ptr(pre), _ptr(slots),
+                                         _ptr(offsets), _ptr(dX), _ptr(dW), _ptr(db), ctypes.c_void_p(p),
+                                         ctypes.c_size_t(n), _stream(dev)))
+    return dX, dW, db
+
+
+def _gates_of(gates, rows, k):
+    if gates is not None:
+        _dev(gates, "gates", torch.float32, (rows, k))
+    return gates
+
+
+def fk_combine(Y, k: int, gates=None, residual=None, out=None):
+    """out[t] = residual[t] + sum_j gates[t, j] Y[t k + j] (gates None: all 1):
+    returns out [rows, d].  Y [rows k, d] is contiguous."""
+    k = int(k)
+    _typed(Y, "Y", _FLOATS)
+    if Y.dim() != 2 or not Y.is_contiguous():
+        raise ValueError("Y must be 2-D and contiguous")
+    if k < 1 or Y.shape[0] % k != 0:
+        raise ValueError(f"Y has {Y.shape[0]} rows, no multiple of k={k}")
+    rows, d = Y.shape[0] // k, Y.shape[1]
+    _gates_of(gates, rows, k)
+    ldr = _rows(residual, "residual", (Y.dtype,), (rows, d)) if residual is not None else d
+    if out is None:
+        out = torch.empty((rows, d), dtype=Y.dtype, device=Y.device)
+    ldo = _rows(out, "out", (Y.dtype,), (rows, d))
+    dev = _one_device(Y, gates, residual, out)
+    with torch.cuda.device(dev):
+        _check(load().fk_combine(DTYPES[Y.dtype], _ptr(Y), rows, k, d, _ptr(gates), _ptr(residual), ldr, _ptr(out),
+                                 ldo, _stream(dev)))
+    return out
+
+
+def fk_combine_backward(dOut, Y, gates):
+    """Gradients of fk_combine: returns (dY [rows k, d], dgates fp32[rows, k])."""
+    ldo = _rows(dOut, "dOut", _FLOATS)
+    rows, d = dOut.shape
+    _dev(gates, "gates", torch.float32)
+    if gates.dim() != 2 or gates.shape[0] != rows:
+        raise ValueError(f"gates has shape {tuple(gates.shape)}, expected ({rows}, k)")
+    k = gates.shape[1]
+    _dev(Y, "Y", dOut.dtype, (rows * k, d))
+    dev = _one_device(dOut, Y, gates)
+    dY = torch.empty((rows * k, d), dtype=dOut.dtype, device=dev)
+    dgates = torch.empty((rows, k), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(load().fk_combine_backward(DTYPES[dOut.dtype], _ptr(dOut), ldo, _ptr(Y), rows, k, d, _ptr(gates),
+                                          _ptr(dY), _ptr(dgates), _stream(dev)))
+    return dY, dgates
 
 
 def fk_profile_enable(on: bool = True):

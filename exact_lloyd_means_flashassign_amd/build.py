@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfk.so")
 OBJDIR = os.path.join(HERE, "_build")
 
-SOURCES = ["fk_api.hip", "fk_assign.hip", "fk_sort.hip", "fk_update.hip"]
+SOURCES = ["fk_api.hip", "fk_assign.hip", "fk_sort.hip", "fk_update.hip", "fk_block_api.hip", "fk_norm.hip",
+           "fk_route.hip", "fk_combine.hip", "fk_linear.hip"]
 # on-box microbenchmarks (HBM stream, row gather, matrix-product loops): a
 # library of their own, loaded only by the benchmark
 MICRO_SOURCE = "fk_micro.hip"

@@ -3,39 +3,17 @@
 // phase timing.  Declared in include/fk.h.
 #include <cmath>
 #include <mutex>
-#include <stdarg.h>
 #include <unordered_map>
-#include <stdio.h>
 #include <string.h>
 #include <vector>
 
 #include "fk.h"
+#include "fk_host.h"
 #include "fk_internal.h"
 
 using namespace fk;
 
 namespace {
-
-thread_local char g_err[512] = "";
-
-fk_status fail(fk_status s, const char *fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return s;
-}
-
-fk_status hip_fail(hipError_t e, const char *what) {
-    (void)hipGetLastError();
-    return fail(FK_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-#define FK_TRY(expr, what)                                  \
-    do {                                                    \
-        hipError_t e_ = (expr);                             \
-        if (e_ != hipSuccess) return hip_fail(e_, (what));  \
-    } while (0)
 
 // Cosine and spherical normalise the rows they compare; spherical also
 // returns unit-length centroids.
@@ -180,30 +158,6 @@ bool known_metric(int32_t metric) {
 
 fk_status check_metric(int32_t metric) {
     if (!known_metric(metric)) return fail(FK_ERR_INVALID_ARG, "unknown metric %d", (int)metric);
-    return FK_OK;
-}
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-bool overlap(const void *a, size_t an, const void *b, size_t bn) {
-    const char *pa = (const char *)a, *pb = (const char *)b;
-    return pa < pb + bn && pb < pa + an;
-}
-
-fk_status check_workspace(void *ws, size_t ws_bytes, size_t need) {
-    if (ws == nullptr) return fail(FK_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
-    if (!aligned(ws, 256)) return fail(FK_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (ws_bytes < need) return fail(FK_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", ws_bytes, need);
-    return FK_OK;
-}
-
-fk_status check_device() {
-    int n = 0;
-    const hipError_t e = hipGetDeviceCount(&n);
-    if (e != hipSuccess || n <= 0) {
-        (void)hipGetLastError();
-        return fail(FK_ERR_NO_DEVICE, "no HIP device is visible");
-    }
     return FK_OK;
 }
 

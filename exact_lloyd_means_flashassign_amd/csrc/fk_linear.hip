@@ -1,0 +1,1070 @@
+// Products with an epilogue for gfx950, and their gradients, for one weight
+// matrix or one per group of rows.
+//
+//   z[p] = X[row(p)] W_g^T + b_g,   Y[slot(p)] = act(z[p]) + R[slot(p)]
+//   dZ = dY act'(z),   dX[slot(p)] = dZ[p] W_g,   dW_g = sum_p dZ[p]^T X[row(p)],   db_g = sum_p dZ[p]
+//
+// p runs over the positions of a slot list sorted by group: slot(p) =
+// slots[p], row(p) = slots[p] / share, and group g owns [offsets[g],
+// offsets[g+1]).  A plain product has one group and slot(p) = row(p) = p.
+#include "fk.h"
+#include "fk_block.h"
+#include "fk_internal.h"
+#include "fk_rows.h"
+
+namespace fk {
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void *lds_ptr;
+typedef const __attribute__((address_space(1))) void *glb_ptr;
+
+// 16 bytes of zeros: what a lane reads in the place of elements past the end
+// of the sum, so that every lane's load stays in bounds.
+__device__ __attribute__((aligned(16))) const uint32_t g_zeros[4] = {0, 0, 0, 0};
+
+// A lane's 16 bytes of an operand for one 32-byte step of the sum, and the
+// products on them: both operands hold the same elements of the sum at the
+// same places, whichever they are.
+template <typename T>
+struct Mma;
+template <>
+struct Mma<__bf16> {
+    typedef v8bf Frag;
+    static __device__ __forceinline__ v16f m32(Frag a, Frag b, v16f c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ v4f m16(Frag a, Frag b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<_Float16> {
+    typedef v8h Frag;
+    static __device__ __forceinline__ v16f m32(Frag a, Frag b, v16f c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ v4f m16(Frag a, Frag b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<float> {
+    typedef v4f Frag;
+    static __device__ __forceinline__ v16f m32(Frag a, Frag b, v16f c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ v4f m16(Frag a, Frag b, v4f c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// ---- activations ----------------------------------------------------------------
+
+// The error function's and tanh's library forms; 1/(1 + e^-z) in a form that
+// does not overflow into NaN (e^-z = inf gives 0).
+__device__ __forceinline__ float activate(int act, float z) {
+    switch (act) {
+    case FK_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case FK_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.707106781f));
+    case FK_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.797884561f * (z + 0.044715f * z * z * z)));
+    case FK_ACT_SILU: return z / (1.0f + expf(-z));
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float act_slope(int act, float z) {
+    switch (act) {
+    case FK_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case FK_ACT_GELU:
+        return 0.5f * (1.0f + erff(z * 0.707106781f)) + z * expf(-0.5f * z * z) * 0.398942280f;
+    case FK_ACT_GELU_TANH: {
+        const float t = tanhf(0.797884561f * (z + 0.044715f * z * z * z));
+        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.797884561f * (1.0f + 0.134145f * z * z);
+    }
+    case FK_ACT_SILU: {
+        const float s = 1.0f / (1.0f + expf(-z));
+        return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+    }
+}
+
+// ---- rows and groups --------------------------------------------------------------
+
+// Where position p lies in a matrix: p itself, or slots[p] / div (a slot out
+// of range is taken as the last one, so that no list can reach past the
+// matrix).
+struct RowMap {
+    const int32_t *slots;
+    int32_t last;        // the largest slot
+    uint32_t mul, shift;  // s / div = (mulhi(s, mul) + s) >> shift for s < 2^31
+    __device__ __forceinline__ int64_t operator()(int64_t p) const {
+        if (slots == nullptr) return p;
+        return of(slots[p]);
+    }
+    __device__ __forceinline__ int64_t of(int32_t s) const {
+        const uint32_t u = (uint32_t)s < (uint32_t)last ? (uint32_t)s : (uint32_t)last;
+        return (__umulhi(u, mul) + u) >> shift;
+    }
+};
+
+RowMap row_map(const int32_t *slots, int64_t M, int div) {
+    RowMap r{slots, (int32_t)(M - 1), 0, 0};
+    while (((int64_t)1 << r.shift) < div) ++r.shift;
+    r.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << r.shift) - (uint64_t)div)) / (uint64_t)div + 1);
+    return r;
+}
+
+// offsets[g] held inside [0, M], rising or not as the caller gave it
+__device__ __forceinline__ int64_t group_at(const int32_t *offsets, int g, int64_t M) {
+    const int32_t o = offsets[g];
+    return o < 0 ? 0 : ((int64_t)o < M ? (int64_t)o : M);
+}
+
+// Finds row tile `want` among the groups' tiles of `rows` rows (groups of
+// `skip` rows or fewer have none).  Group G stands for the positions past the
+// last group (with_rest).  Every lane of a wave calls it and gets the same
+// answer.  Returns the number of tiles in all; g = -1 if there is no such tile.
+struct TileAt {
+    int g;
+    int64_t p0, p1;  // its positions
+};
+__device__ __forceinline__ int64_t find_tile(const int32_t *offsets, int G, int64_t M, int rows, int skip,
+                                             bool with_rest, int64_t want, TileAt &t) {
+    t.g = -1;
+    t.p0 = t.p1 = 0;
+    const int lane = threadIdx.x & 63;
+    const int n = G + (with_rest ? 1 : 0);
+    int64_t before = 0;
+    for (int g0 = 0; g0 < n; g0 += 64) {
+        const int g = g0 + lane;
+        int64_t a = 0, b = 0;
+        if (g < n) {
+            a = group_at(offsets, g, M);
+            b = g < G ? group_at(offsets, g + 1, M) : M;
+        }
+        const int64_t cnt = b > a ? b - a : 0;
+        const int tiles = g < G && cnt <= skip ? 0 : (int)((cnt + rows - 1) / rows);
+        int inc = tiles;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int up = __shfl_up(inc, o, 64);
+            if (lane >= o) inc += up;
+        }
+        const int64_t mine = before + inc - tiles;
+        const uint64_t hit = __ballot(want >= mine && want < mine + tiles);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            const int64_t first = __shfl(mine, src, 64);
+            const int64_t ga = __shfl(a, src, 64), gb = __shfl(b, src, 64);
+            t.g = g0 + src;
+            t.p0 = ga + (want - first) * rows;
+            t.p1 = t.p0 + rows < gb ? t.p0 + rows : gb;
+        }
+        before += __shfl(inc, 63, 64);
+    }
+    return before;
+}
+
+// The tile of this workgroup when `total` of them are spread over the 8 XCDs,
+// which take workgroups in turn: each XCD gets a run of consecutive tiles, so
+// that the tiles that share operands share an L2.  -1: none.
+__device__ __forceinline__ int64_t xcd_tile(int64_t id, int64_t total) {
+    const int64_t x = id & 7, i = id >> 3, q = total >> 3, r = total & 7;
+    if (i >= q + (x < r ? 1 : 0)) return -1;
+    return x * q + (x < r ? x : r) + i;
+}
+
+// ---- the tiled product -------------------------------------------------------------
+
+enum { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct LinArgs {
+    const void *A, *B;
+    void *C, *Z;
+    const void *bias, *R;
+    float *part;  // split sums: [splits][rows of C in position order][N]
+    const int32_t *offsets;
+    RowMap amap, bmap, cmap;
+    int64_t lda, ldb, ldc, ldz, ldr;
+    int64_t gsb, gsc, gsbias;  // group strides of B, C, bias
+    int64_t M;                 // positions
+    int64_t rows, N;           // rows (of a group for kDw) and columns of C
+    int64_t ka, kb;            // where the sum ends in A and in B
+    int G, act, splits, skip, cf32, bf32;
+};
+
+// One operand's tile: ROWS rows (or columns) of C by 128 bytes of the sum, in
+// LDS as 16-byte chunks.
+//   KM (the sum is contiguous in memory): LDS row r holds 8 chunks, chunk c at
+//     place c ^ (r & 7): the 8 lanes that read a chunk of 8 consecutive rows
+//     meet 8 different places.
+//   otherwise (rows of the operand are steps of the sum): LDS row k holds the
+//     tile's columns, chunk c at place c ^ ((k & 3) << 2): the four rows that a
+//     transposing read takes lie 64 bytes apart.
+// Loads go from memory straight to LDS, 16 bytes a lane, each lane fetching
+// the chunk that belongs at its place.
+template <typename T, bool KM, int ROWS, int NT>
+struct Operand {
+    static constexpr int E = 16 / (int)sizeof(T);       // elements a chunk
+    static constexpr int IT = ROWS * 8 / NT;            // loads a thread
+    static constexpr int CPR = KM ? 8 : ROWS / E;       // chunks a LDS row
+    static constexpr int STEP = NT / CPR;               // LDS rows a load of all threads covers
+    const T *p[KM ? IT : 1];
+    int kofs;       // KM: this thread's chunk in the 128 bytes; else its row of the sum
+    int64_t ld;
+    int32_t idx[KM ? 1 : IT];
+    RowMap map;
+    int64_t pos0;
+
+    // KM: rows [r0, r0 + n) of C at positions; out of range rows repeat the last
+    __device__ __forceinline__ void init_km(const T *base, int64_t ld_, const RowMap &m, int64_t r0, int64_t n) {
+        const int row = threadIdx.x >> 3;
+        kofs = ((threadIdx.x & 7) ^ (row & 7)) * E;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int64_t r = row + i * STEP;
+            p[i] = base + m(r0 + (r < n ? r : n - 1)) * ld_ + kofs;
+        }
+    }
+    // not KM: columns [c0, cols), the sum over positions from pos
+    __device__ __forceinline__ void init_mn(const T *base, int64_t ld_, const RowMap &m, int64_t c0, int64_t cols,
+                                            int64_t pos) {
+        kofs = threadIdx.x / CPR;
+        const int64_t c = c0 + (int64_t)((threadIdx.x % CPR) ^ ((kofs & 3) << 2)) * E;
+        const int64_t lastc = (cols - 1) / E * E;
+        p[0] = base + (c < lastc ? c : lastc);
+        ld = ld_;
+        map = m;
+        pos0 = pos;
+    }
+    // not KM: the slots of the next tile of the sum
+    __device__ __forceinline__ void fetch_rows(int64_t k0, int64_t kend) {
+        if constexpr (!KM) {
+            if (map.slots != nullptr) {
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const int64_t k = k0 + kofs + i * STEP;
+                    idx[i] = map.slots[pos0 + (k < kend ? k : kend - 1)];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void issue(int64_t k0, int64_t kend, T *lds, int wave) const {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const void *src;
+            if constexpr (KM) {
+                src = k0 + kofs < kend ? (const void *)(p[i] + k0) : (const void *)g_zeros;
+            } else {
+                const int64_t k = k0 + kofs + i * STEP;
+                const int64_t r = map.slots != nullptr ? map.of(idx[i]) : pos0 + k;
+                src = k < kend ? (const void *)(p[0] + r * ld) : (const void *)g_zeros;
+            }
+            __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(lds + (i * NT + wave * 64) * E), 16, 0, 0);
+        }
+    }
+    // The lane's 16 bytes for rows (columns) [r0, r0 + 32) and 32-byte step s
+    __device__ __forceinline__ static typename Mma<T>::Frag frag(const T *lds, int r0, int s) {
+        const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+        if constexpr (KM) {
+            const int r = r0 + l;
+            return *reinterpret_cast<const typename Mma<T>::Frag *>(lds + (r * 8 + ((s * 2 + h) ^ (r & 7))) * E);
+        } else if constexpr (sizeof(T) == 4) {
+            typename Mma<T>::Frag f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = s * 8 + h * 4 + i, c = r0 + l;
+                f[i] = lds[k * ROWS + ((c / E) ^ ((k & 3) << 2)) * E + c % E];
+            }
+            return f;
+        } else {
+            // groups of 16 lanes read 4 rows of 16 columns and get a column
+            // (4 steps of the sum) each
+            const int i = lane & 15, c = r0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
+            const int k = s * 16 + h * 8 + (i >> 2);
+            const T *q = lds + k * ROWS + ((c / E) ^ ((k & 3) << 2)) * E + c % E;
+            typedef __attribute__((address_space(3))) v4s *P;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * ROWS));
+            const v8s both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(typename Mma<T>::Frag, both);
+        }
+    }
+};
+
+// Eight neighbouring values of a row of C through the epilogue and out.
+template <typename T>
+struct Epilogue {
+    float bias[8];
+    int64_t col;
+    int n;  // columns of the eight that exist
+    __device__ __forceinline__ void init(const LinArgs &a, int g, int64_t c) {
+        col = c;
+        const int64_t left = a.N - c;
+        n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            bias[i] = 0.0f;
+            if (a.bias != nullptr && i < n) {
+                const int64_t at = (int64_t)g * a.gsbias + c + i;
+                bias[i] = a.bf32 ? ((const float *)a.bias)[at] : (float)((const T *)a.bias)[at];
+            }
+        }
+    }
+    static __device__ __forceinline__ void put(T *q, const float (&v)[8], int n) {
+        constexpr int E = 16 / (int)sizeof(T);
+        if (n == 8 && ((uintptr_t)q & 15) == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; j += E) {
+                Chunk<T, E> o;
+#pragma unroll
+                for (int i = 0; i < E; ++i) o.e[i] = (T)v[j + i];
+                o.store(q + j);
+            }
+        } else {
+            for (int i = 0; i < 8; ++i)
+                if (i < n) q[i] = (T)v[i];
+        }
+    }
+    static __device__ __forceinline__ void get(const T *q, float (&v)[8], int n) {
+        constexpr int E = 16 / (int)sizeof(T);
+        if (n == 8 && ((uintptr_t)q & 15) == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; j += E) {
+                Chunk<T, E> o;
+                o.load(q + j);
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[j + i] = (float)o.e[i];
+            }
+        } else {
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)q[i] : 0.0f;
+        }
+    }
+    // crow: the row of C (kDw: within its group)
+    __device__ __forceinline__ void out(const LinArgs &a, int g, int64_t crow, float (&v)[8]) const {
+        if (n == 0) return;
+        const int64_t at = (int64_t)g * a.gsc + crow * a.ldc + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += bias[i];
+        if (a.Z != nullptr) put((T *)a.Z + crow * a.ldz + col, v, n);
+        if (a.act != FK_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = activate(a.act, v[i]);
+        }
+        if (a.R != nullptr) {
+            float r[8];
+            get((const T *)a.R + crow * a.ldr + col, r, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        if (a.cf32) Epilogue<float>::put((float *)a.C + at, v, n);
+        else put((T *)a.C + at, v, n);
+    }
+};
+
+// BM x BN of C a workgroup of WM x WN waves, 128 bytes of the sum a step, two
+// tiles of each operand in LDS: one is multiplied while the next one's loads
+// are in flight.
+template <typename T, int KIND, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtiles, int64_t ntiles) {
+    constexpr int NT = WM * WN * 64;
+    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int BK = 8 * E;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+    static_assert(BN / WN == 64, "the epilogue stages 64 columns a wave");
+    constexpr bool AKM = KIND != kDw, BKM = KIND == kFwd;
+    __shared__ __attribute__((aligned(16))) T sA0[BM * BK];
+    __shared__ __attribute__((aligned(16))) T sA1[BM * BK];
+    __shared__ __attribute__((aligned(16))) T sB0[BN * BK];
+    __shared__ __attribute__((aligned(16))) T sB1[BN * BK];
+
+    // ---- which tile ----
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int split = blockIdx.y;
+    TileAt t{0, 0, 0};
+    int64_t nt, r0, nrows;   // column tile; first row of C and rows of it in the tile
+    int64_t kbeg = 0, ka = a.ka, kb = a.kb;
+    int64_t pos = 0;         // kDw: the group's first position
+    if constexpr (KIND == kDw) {
+        const int64_t per = mtiles * ntiles;
+        const int64_t id = xcd_tile(blockIdx.x, per * a.G);
+        t.g = (int)(id / per);
+        const int64_t in = id % per;
+        nt = in % ntiles;
+        r0 = in / ntiles * BM;
+        nrows = a.rows - r0 < BM ? a.rows - r0 : BM;
+        int64_t p1 = a.M;
+        if (a.offsets != nullptr) {
+            pos = group_at(a.offsets, t.g, a.M);
+            p1 = group_at(a.offsets, t.g + 1, a.M);
+        }
+        ka = kb = p1 > pos ? p1 - pos : 0;
+    } else if (a.offsets == nullptr) {
+        // runs of 8 row tiles by all column tiles
+        const int64_t id = xcd_tile(blockIdx.x, mtiles * ntiles);
+        constexpr int GM = 8;
+        const int64_t strip = id / (GM * ntiles), in = id % (GM * ntiles);
+        const int64_t gm = mtiles - strip * GM < GM ? mtiles - strip * GM : GM;
+        nt = in / gm;
+        r0 = (strip * GM + in % gm) * BM;
+        nrows = a.rows - r0 < BM ? a.rows - r0 : BM;
+    } else {
+        // only the workgroups that have a tile come past this (no barrier yet)
+        const bool rest = a.splits == 1;
+        TileAt none;
+        const int64_t tiles = find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, -1, none);
+        const int64_t id = xcd_tile(blockIdx.x, tiles * ntiles);
+        if (id < 0) return;
+        nt = id % ntiles;
+        find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, id / ntiles, t);
+        r0 = t.p0;
+        nrows = t.p1 - t.p0;
+    }
+    const int64_t c0 = nt * BN;
+    const bool rest = KIND != kDw && a.offsets != nullptr && t.g == a.G;
+
+    // the part of the sum that this split takes
+    const int64_t kall = ka > kb ? ka : kb;
+    int64_t steps = (kall + BK - 1) / BK;
+    if (a.splits > 1) {
+        const int64_t each = (steps + a.splits - 1) / a.splits;
+        kbeg = split * each * BK;
+        const int64_t left = steps - split * each;
+        steps = left < each ? (left > 0 ? left : 0) : each;
+    }
+    if (rest) steps = 0;
+
+    Operand<T, AKM, BM, NT> oa;
+    Operand<T, BKM, BN, NT> ob;
+    const T *Bg = (const T *)a.B + (KIND == kDw || rest ? 0 : (int64_t)t.g * a.gsb);
+    if constexpr (AKM) oa.init_km((const T *)a.A, a.lda, a.amap, r0, nrows);
+    else oa.init_mn((const T *)a.A, a.lda, a.amap, r0, a.rows, pos);
+    if constexpr (BKM) {
+        const RowMap id{nullptr, 0, 0, 0};
+        ob.init_km(Bg, a.ldb, id, c0, a.N - c0 < BN ? a.N - c0 : BN);
+    } else {
+        ob.init_mn(Bg, a.ldb, a.bmap, c0, a.N, pos);
+    }
+
+    v16f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+    auto issue = [&](int64_t k0, T *sa, T *sb) {
+        oa.issue(k0, ka, sa, wave);
+        ob.issue(k0, kb, sb, wave);
+    };
+    auto rows_ahead = [&](int64_t k0) {
+        oa.fetch_rows(k0, ka);
+        ob.fetch_rows(k0, kb);
+    };
+    auto multiply = [&](const T *sa, const T *sb) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            typename Mma<T>::Frag fa[TM], fb[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[j] = ob.frag(sb, wn + j * 32, s);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = oa.frag(sa, wm + i * 32, s);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::m32(fb[j], fa[i], acc[i][j]);
+        }
+    };
+    if (steps > 0) {
+        rows_ahead(kbeg);
+        issue(kbeg, sA0, sB0);
+        rows_ahead(kbeg + BK);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        for (int64_t st = 0; st < steps; st += 2) {
+            const int64_t k = kbeg + st * BK;
+            if (st + 1 < steps) {
+                issue(k + BK, sA1, sB1);
+                rows_ahead(k + 2 * BK);
+            }
+            multiply(sA0, sB0);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (st + 1 >= steps) break;
+            if (st + 2 < steps) {
+                issue(k + 2 * BK, sA0, sB0);
+                rows_ahead(k + 3 * BK);
+            }
+            multiply(sA1, sB1);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+        }
+    }
+
+    // ---- out: 32 rows of 64 columns a wave at a time through LDS, so that the
+    // rows leave in whole chunks.  A lane holds one row of C and 4 columns
+    // apiece of it (the operands are multiplied the other way round).
+    constexpr int LDS_ROW = 68;
+    constexpr int PER = NT / 256;  // waves that stage in one of the four tiles
+    static_assert(PER * 32 * LDS_ROW * 4 <= BM * 128 && BM == BN, "the staged rows fit the tiles");
+    const int at = wave / PER;
+    float *stage = reinterpret_cast<float *>(at == 0 ? sA0 : at == 1 ? sA1 : at == 2 ? sB0 : sB1) +
+                   wave % PER * 32 * LDS_ROW;
+    const int lane = threadIdx.x & 63;
+    Epilogue<T> ep;
+    const int64_t col = c0 + wn + (lane & 7) * 8;
+    if (a.splits > 1 || rest) {
+        ep.col = col;
+        const int64_t left = a.N - col;
+        ep.n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    } else {
+        ep.init(a, t.g, col);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v4f v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][q * 4 + e];
+                *reinterpret_cast<v4f *>(stage + (lane & 31) * LDS_ROW + j * 32 + q * 8 + (lane >> 5) * 4) = v;
+            }
+        // the wave's own region: its lanes' writes before its lanes' reads
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            const int row = q * 8 + (lane >> 3);
+            const int64_t r = wm + i * 32 + row;
+            float v[8];
+            const v4f lo = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + (lane & 7) * 8);
+            const v4f hi = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + (lane & 7) * 8 + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = lo[e];
+                v[4 + e] = hi[e];
+            }
+            if (r < nrows) {
+                if (a.splits > 1) {
+                    const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
+                    const int64_t prow = KIND == kDw ? (int64_t)t.g * a.rows + r0 + r : r0 + r;
+                    Epilogue<float>::put(a.part + ((int64_t)split * all + prow) * a.N + ep.col, v, ep.n);
+                } else if (rest) {
+                    const int64_t crow = a.cmap(r0 + r);
+                    if (a.cf32) Epilogue<float>::put((float *)a.C + crow * a.ldc + col, v, ep.n);
+                    else Epilogue<T>::put((T *)a.C + crow * a.ldc + col, v, ep.n);
+                    if (a.Z != nullptr) Epilogue<T>::put((T *)a.Z + crow * a.ldz + col, v, ep.n);
+                } else {
+                    ep.out(a, KIND == kDw || a.offsets == nullptr ? (KIND == kDw ? t.g : 0) : t.g,
+                           KIND == kDw ? r0 + r : a.cmap(r0 + r), v);
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Adds the partial products of a split sum and runs the epilogue: 8 columns a
+// thread, the splits in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
+    const int64_t all = kind == kDw ? (int64_t)a.G * a.rows : a.M;
+    const int64_t chunks = (a.N + 7) / 8;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= all * chunks) return;
+    const int64_t r = id / chunks, col = id % chunks * 8;
+    int g = 0;
+    int64_t crow = r;
+    bool rest = false;
+    if (kind == kDw) {
+        g = (int)(r / a.rows);
+        crow = r % a.rows;
+    } else {
+        crow = a.cmap(r);
+        if (a.offsets != nullptr) {
+            // the last group that starts at or before r and is not empty
+            int lo = 0, hi = a.G;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (group_at(a.offsets, mid + 1, a.M) <= r) lo = mid + 1;
+                else hi = mid;
+            }
+            g = lo;
+            rest = g >= a.G;
+            if (!rest) {
+                const int64_t n = group_at(a.offsets, g + 1, a.M) - group_at(a.offsets, g, a.M);
+                if (n <= a.skip) return;
+            }
+        }
+    }
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    Epilogue<T> ep;
+    if (rest) {
+        ep.n = a.N - col >= 8 ? 8 : (int)(a.N - col);
+        if (a.cf32) Epilogue<float>::put((float *)a.C + crow * a.ldc + col, v, ep.n);
+        else Epilogue<T>::put((T *)a.C + crow * a.ldc + col, v, ep.n);
+        if (a.Z != nullptr) Epilogue<T>::put((T *)a.Z + crow * a.ldz + col, v, ep.n);
+        return;
+    }
+    ep.init(a, g, col);
+    for (int s = 0; s < a.splits; ++s) {
+        float w[8];
+        Epilogue<float>::get(a.part + ((int64_t)s * all + r) * a.N + col, w, ep.n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    ep.out(a, g, crow, v);
+}
+
+// ---- a few rows against a whole weight matrix -----------------------------------------
+//
+// Bound by the stream of the weights.  A workgroup takes 16 rows of W (columns
+// of C); its waves take every WV-th 128-byte stretch of the sum each and read W
+// straight into the matrix instruction's registers, 16 bytes a lane, eight
+// stretches' halves in flight; the rows of X come from cache.  The waves'
+// sums are added in wave order through LDS.  Groups of more than 16 MT rows
+// are left to the tiled product (dense: there are none).
+template <typename T, int MT, int WV, bool WIDE>
+__global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
+    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int STEP = 4 * E;  // elements of the sum in one load of a wave
+    __shared__ float sm[WV][MT * 16][17];
+    const int g = blockIdx.y;
+    int64_t p0 = 0, cnt = a.M;
+    if (a.offsets != nullptr) {
+        p0 = group_at(a.offsets, g, a.M);
+        cnt = group_at(a.offsets, g + 1, a.M) - p0;
+        if (cnt <= 0 || cnt > a.skip) return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n = n0 + l < a.N ? n0 + l : a.N - 1;
+    const T *w = (const T *)a.B + (int64_t)g * a.gsb + n * a.ldb;
+    const T *x[MT];
+    bool xin[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        xin[t] = t * 16 + l < cnt;
+        x[t] = (const T *)a.A + a.amap(p0 + (xin[t] ? t * 16 + l : 0)) * a.lda;
+    }
+    v4f acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    typedef typename Mma<T>::Frag Frag;
+    const int K = (int)a.ka;
+    auto load = [&](const T *p, int k, bool in) {
+        Frag f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = (T)0.0f;
+        if constexpr (WIDE) {
+            if (in && k < K) f = *reinterpret_cast<const Frag *>(p + k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (in && k + i < K) f[i] = p[k + i];
+        }
+        return f;
+    };
+    constexpr int U = 4;  // loads of W a wave has in flight
+    for (int k0 = wave * STEP * U; k0 < K; k0 += WV * STEP * U) {
+        Frag fw[U], fx[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) fw[u] = load(w, k0 + u * STEP + q * E, true);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) fx[u][t] = load(x[t], k0 + u * STEP + q * E, xin[t]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[t] = Mma<T>::m16(fw[u], fx[u][t], acc[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sm[wave][t * 16 + l][q * 4 + i] = acc[t][i];
+    __syncthreads();
+    // 8 columns a thread
+    for (int i = threadIdx.x; i < MT * 32; i += WV * 64) {
+        const int m = i >> 1, c = (i & 1) * 8;
+        if (m >= cnt) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = 0.0f;
+            for (int k = 0; k < WV; ++k) v[e] += sm[k][m][c + e];
+        }
+        Epilogue<T> ep;
+        ep.init(a, g, n0 + c);
+        ep.out(a, g, a.cmap(p0 + m), v);
+    }
+}
+
+// ---- the backward pass's element-wise step ----------------------------------------------
+//
+// dZ[p] = dY[slot(p)] act'(z[slot(p)]) in position order, rounded to the type
+// that the matrix instructions take (and padded with zeros to whole chunks),
+// and the partial column sums of the unrounded values for db: one row tile of
+// one group and 8 columns a thread.
+constexpr int kGradRows = 64;
+template <typename T>
+__global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int64_t ldd, int df32, T *dZ, int64_t lddz,
+                                                  float *colsum) {
+    __shared__ float sm[8][256];
+    TileAt t{0, 0, 0};
+    if (a.offsets == nullptr) {
+        t.p0 = (int64_t)blockIdx.x * kGradRows;
+        t.p1 = t.p0 + kGradRows < a.M ? t.p0 + kGradRows : a.M;
+    } else {
+        find_tile(a.offsets, a.G, a.M, kGradRows, 0, false, blockIdx.x, t);
+        if (t.g < 0) return;
+    }
+    // 32 threads across 256 columns, 8 rows at a time
+    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.y * 256 + cx * 8;
+    const int n = a.N - col >= 8 ? 8 : (a.N > col ? (int)(a.N - col) : 0);
+    const int npad = lddz - col >= 8 ? 8 : (lddz > col ? (int)(lddz - col) : 0);
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (n > 0 || (dZ != nullptr && npad > 0)) {
+        for (int64_t p = t.p0 + ry; p < t.p1; p += 8) {
+            const int64_t row = a.cmap(p);
+            float d[8];
+            if (df32) Epilogue<float>::get((const float *)dY + row * ldd + col, d, n);
+            else Epilogue<T>::get((const T *)dY + row * ldd + col, d, n);
+            if (a.act != FK_ACT_NONE) {
+                float z[8];
+                Epilogue<T>::get((const T *)a.Z + row * a.ldz + col, z, n);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] *= act_slope(a.act, z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] = i < n ? d[i] : 0.0f;
+                s[i] += d[i];
+            }
+            if (dZ != nullptr) Epilogue<T>::put(dZ + p * lddz + col, d, npad);
+        }
+    }
+    if (colsum == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sm[ry][cx * 8 + i] = s[i];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    if (c < a.N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += sm[i][threadIdx.x];
+        colsum[(int64_t)blockIdx.x * a.N + c] = v;
+    }
+}
+
+// db of one group: its row tiles' column sums in order, 16 threads down a column
+template <typename T>
+__global__ __launch_bounds__(256) void k_bias_grad(LinArgs a, const float *colsum, void *db, int f32) {
+    __shared__ float sm[16][17];
+    __shared__ int64_t range[2];
+    const int g = blockIdx.y;
+    if (threadIdx.x < 64) {
+        int64_t first = 0, tiles;
+        if (a.offsets == nullptr) {
+            tiles = (a.M + kGradRows - 1) / kGradRows;
+        } else {
+            // the row tiles of the groups before this one
+            int64_t s = 0;
+            for (int i = threadIdx.x; i < g; i += 64) {
+                const int64_t c = group_at(a.offsets, i + 1, a.M) - group_at(a.offsets, i, a.M);
+                s += c > 0 ? (c + kGradRows - 1) / kGradRows : 0;
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+            first = s;
+            const int64_t c = group_at(a.offsets, g + 1, a.M) - group_at(a.offsets, g, a.M);
+            tiles = c > 0 ? (c + kGradRows - 1) / kGradRows : 0;
+        }
+        if (threadIdx.x == 0) {
+            range[0] = first;
+            range[1] = first + tiles;
+        }
+    }
+    __syncthreads();
+    const int col = threadIdx.x & 15, down = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + col;
+    float s = 0.0f;
+    if (c < a.N) {
+#pragma unroll 4
+        for (int64_t p = range[0] + down; p < range[1]; p += 16) s += colsum[p * a.N + c];
+    }
+    sm[down][col] = s;
+    __syncthreads();
+    if (down == 0 && c < a.N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += sm[i][col];
+        const int64_t at = (int64_t)g * a.N + c;
+        if (f32) ((float *)db)[at] = v;
+        else ((T *)db)[at] = (T)v;
+    }
+}
+
+// out[r] = in[r] with its columns padded by zeros to ldo (whole chunks): the
+// tiled product reads 16 bytes at a time, so operands whose rows do not start
+// on 16 bytes are laid out once more first.
+template <typename T>
+__global__ __launch_bounds__(256) void k_pad_rows(const T *in, int64_t ldi, int64_t rows, int64_t cols, T *out,
+                                                  int64_t ldo) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int64_t chunks = ldo / E;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < rows * chunks; id += (int64_t)gridDim.x * 256) {
+        const int64_t r = id / chunks, c = id % chunks * E;
+        Chunk<T, E> o;
+#pragma unroll
+        for (int i = 0; i < E; ++i) o.e[i] = c + i < cols ? in[r * ldi + c + i] : (T)0.0f;
+        o.store(out + r * ldo + c);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+constexpr int kFewRows = 16;      // most rows of a group that k_product_few takes
+constexpr int kCus = 256;
+
+template <typename T, int KIND>
+hipError_t run_product(const LinArgs &a, int tile, hipStream_t s) {
+    const int64_t nt = cdiv(a.N, tile);
+    int64_t mt, grid;
+    if (KIND == kDw) {
+        mt = cdiv(a.rows, tile);
+        grid = mt * nt * a.G;
+    } else if (a.offsets == nullptr) {
+        mt = cdiv(a.rows, tile);
+        grid = mt * nt;
+    } else {
+        // the groups that have tiles hold more than skip rows each
+        const int64_t most = a.M / (a.skip + 1);
+        mt = a.M / tile + (most < a.G ? most : a.G) + 1;
+        grid = mt * nt;
+    }
+    if (grid > 0) {
+        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        const dim3 gr((unsigned)grid, (unsigned)a.splits);
+        if (tile == 256) k_product<T, KIND, 256, 256, 2, 4><<<gr, 512, 0, s>>>(a, mt, nt);
+        else k_product<T, KIND, 128, 128, 2, 2><<<gr, 256, 0, s>>>(a, mt, nt);
+    }
+    if (a.splits > 1) {
+        const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
+        const int64_t n = cdiv(all * cdiv(a.N, 8), 256);
+        if (n > INT32_MAX) return hipErrorInvalidValue;
+        if (n > 0) k_join<T><<<(unsigned)n, 256, 0, s>>>(a, KIND);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, bool WIDE>
+hipError_t run_few(const LinArgs &a, hipStream_t s) {
+    const dim3 gr((unsigned)cdiv(a.N, 16), (unsigned)(a.offsets ? a.G : 1));
+    k_product_few<T, 1, 4, WIDE><<<gr, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+// Tile and splits of a product with `mt` x `nt` x `groups` tiles of 256 and a
+// sum of `steps` 128-byte steps.
+struct Shape {
+    int tile, splits;
+};
+Shape pick_shape(int64_t rows, int64_t cols, int64_t groups, int64_t steps) {
+    Shape s;
+    const int64_t big = cdiv(rows, 256) * cdiv(cols, 256) * groups;
+    s.tile = rows > 128 && big >= kCus * 3 / 4 ? 256 : 128;
+    const int64_t tiles = cdiv(rows, s.tile) * cdiv(cols, s.tile) * groups;
+    s.splits = 1;
+    while (s.splits < 16 && tiles * s.splits * 2 <= kCus && steps / (s.splits * 2) >= 4) s.splits *= 2;
+    return s;
+}
+
+size_t pad16(int64_t rows, int64_t cols, int dtype) {
+    const int64_t e = 16 / (int64_t)dtype_size(dtype);
+    return align_up((size_t)rows * (size_t)(cdiv(cols, e) * e) * dtype_size(dtype), 256);
+}
+
+bool whole(int64_t cols, int64_t ld, int dtype) {
+    const int64_t e = 16 / (int64_t)dtype_size(dtype);
+    return cols % e == 0 && ld % e == 0;
+}
+
+}  // namespace
+
+// What a call needs and in which order its scratch is laid out.
+LinearPlan plan_linear(const LinearShape &h, bool backward) {
+    LinearPlan p{};
+    p.M = h.M, p.G = h.grouped ? h.G : 0;
+    const int64_t groups = h.grouped ? h.G : 1;
+    const int64_t bk = 128 / (int64_t)dtype_size(h.dtype);
+    const int64_t mean = h.grouped ? cdiv(h.M, h.G) : h.M;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += align_up(bytes > 0 ? bytes : 1, 256);
+        return o;
+    };
+    p.few = !backward && mean <= kFewRows;
+    p.tiled = backward || h.grouped || !p.few;
+    p.pad_x = p.tiled && !whole(h.K, h.ldx, h.dtype);
+    p.pad_w = p.tiled && !whole(h.K, h.ldw, h.dtype);
+    const int64_t wrows = groups * h.N;
+    if (p.pad_x) p.xpad = take(pad16(h.M / h.share, h.K, h.dtype));
+    if (p.pad_w) p.wpad = take(pad16(wrows, h.K, h.dtype));
+    if (!backward) {
+        const Shape s = pick_shape(h.grouped ? mean : h.M, h.N, groups, cdiv(h.K, bk));
+        p.tile = s.tile, p.splits = s.splits;
+        if (p.tiled && p.splits > 1) p.part = take((size_t)p.splits * h.M * h.N * 4);
+        p.total = off > 0 ? off : 256;
+        return p;
+    }
+    // dZ is laid out in position order unless dY serves as it is
+    p.make_dz = h.act != FK_ACT_NONE || h.ydtype != h.dtype || !whole(h.N, h.ldy, h.dtype);
+    if (p.make_dz) p.dz = take(pad16(h.M, h.N, h.dtype));
+    p.grad_tiles = h.grouped ? h.M / kGradRows + (h.G < h.M ? h.G : h.M) : cdiv(h.M, kGradRows);
+    p.colsum = take((size_t)p.grad_tiles * h.N * 4);
+    const Shape sx = pick_shape(h.grouped ? mean : h.M, h.K, groups, cdiv(h.N, bk));
+    const Shape sw = pick_shape(h.N, h.K, groups, cdiv(mean, bk));
+    p.tile = sx.tile, p.splits = sx.splits, p.tile_w = sw.tile, p.splits_w = sw.splits;
+    const size_t px = p.splits > 1 ? (size_t)p.splits * h.M * h.K * 4 : 0;
+    const size_t pw = p.splits_w > 1 ? (size_t)p.splits_w * wrows * h.K * 4 : 0;
+    p.part = take(px > pw ? px : pw);
+    p.total = off;
+    return p;
+}
+
+namespace {
+
+template <typename T>
+hipError_t pad_rows(const void *in, int64_t ldi, int64_t rows, int64_t cols, void *out, hipStream_t s) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int64_t ldo = cdiv(cols, E) * E;
+    const int64_t n = cdiv(rows * (ldo / E), 256);
+    if (n > 0) k_pad_rows<T><<<(unsigned)(n < 65536 ? n : 65536), 256, 0, s>>>((const T *)in, ldi, rows, cols, (T *)out, ldo);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t linear_fwd(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, char *ws, hipStream_t s) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int64_t kp = cdiv(h.K, E) * E;
+    LinArgs a{};
+    a.bias = b.bias, a.R = b.R, a.C = b.Y, a.Z = b.Z;
+    a.bf32 = h.bias_f32, a.cf32 = h.ydtype == FK_F32;
+    a.ldc = h.ldy, a.ldz = h.ldz, a.ldr = h.ldr;
+    a.gsbias = h.N;
+    a.offsets = b.offsets;
+    a.amap = row_map(b.slots, h.M, h.share);
+    a.cmap = row_map(b.slots, h.M, 1);
+    a.M = a.rows = h.M, a.N = h.N, a.G = h.grouped ? h.G : 1, a.act = h.act, a.splits = p.splits;
+    a.part = (float *)(ws + p.part);
+    hipError_t e = hipSuccess;
+    if (p.few) {
+        a.A = b.X, a.lda = h.ldx, a.B = b.W, a.ldb = h.ldw, a.gsb = h.N * h.ldw, a.ka = a.kb = h.K;
+        a.skip = kFewRows;
+        e = whole(h.K, h.ldx, h.dtype) && whole(h.K, h.ldw, h.dtype) ? run_few<T, true>(a, s) : run_few<T, false>(a, s);
+        if (e != hipSuccess || !p.tiled) return e;
+    }
+    a.skip = p.few ? kFewRows : 0;
+    a.A = b.X, a.lda = h.ldx, a.B = b.W, a.ldb = h.ldw, a.gsb = h.N * h.ldw;
+    a.ka = a.kb = kp;
+    if (p.pad_x) {
+        if ((e = pad_rows<T>(b.X, h.ldx, h.M / h.share, h.K, ws + p.xpad, s)) != hipSuccess) return e;
+        a.A = ws + p.xpad, a.lda = kp;
+    }
+    if (p.pad_w) {
+        e = pad_rows<T>(b.W, h.ldw, a.G * h.N, h.K, ws + p.wpad, s);
+        if (e != hipSuccess) return e;
+        a.B = ws + p.wpad, a.ldb = kp, a.gsb = h.N * kp;
+    }
+    return run_product<T, kFwd>(a, p.tile, s);
+}
+
+template <typename T>
+hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, char *ws, hipStream_t s) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int64_t kp = cdiv(h.K, E) * E, np = cdiv(h.N, E) * E;
+    const int G = h.grouped ? h.G : 1;
+    hipError_t e = hipSuccess;
+    LinArgs c{};
+    c.offsets = b.offsets, c.cmap = row_map(b.slots, h.M, 1), c.M = h.M, c.N = h.N, c.G = G, c.act = h.act;
+    c.Z = (void *)b.Zin, c.ldz = h.ldz;
+    if ((p.make_dz && (b.dX || b.dW)) || b.db) {
+        T *dz = p.make_dz && (b.dX || b.dW) ? (T *)(ws + p.dz) : nullptr;
+        float *cs = b.db ? (float *)(ws + p.colsum) : nullptr;
+        if (p.grad_tiles > 0) {
+            k_act_grad<T><<<dim3((unsigned)p.grad_tiles, (unsigned)cdiv(h.N, 256)), 256, 0, s>>>(
+                c, b.dY, h.ldy, h.ydtype == FK_F32, dz, np, cs);
+        }
+        if (b.db)
+            k_bias_grad<T><<<dim3((unsigned)cdiv(h.N, 16), (unsigned)G), 256, 0, s>>>(c, cs, b.db, h.bias_f32);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const void *X = b.X, *W = b.W;
+    int64_t ldx = h.ldx, ldw = h.ldw;
+    if (p.pad_x && b.dW) {
+        if ((e = pad_rows<T>(X, ldx, h.M / h.share, h.K, ws + p.xpad, s)) != hipSuccess) return e;
+        X = ws + p.xpad, ldx = kp;
+    }
+    if (p.pad_w && b.dX) {
+        if ((e = pad_rows<T>(W, ldw, G * h.N, h.K, ws + p.wpad, s)) != hipSuccess) return e;
+        W = ws + p.wpad, ldw = kp;
+    }
+    LinArgs a{};
+    a.offsets = b.offsets, a.M = h.M, a.G = G, a.act = FK_ACT_NONE, a.part = (float *)(ws + p.part);
+    a.A = p.make_dz ? ws + p.dz : b.dY;
+    a.lda = p.make_dz ? np : h.ldy;
+    a.amap = row_map(p.make_dz ? nullptr : b.slots, h.M, 1);
+    if (b.dX) {
+        a.B = W, a.ldb = ldw, a.gsb = h.N * ldw, a.bmap = row_map(nullptr, h.M, 1);
+        a.C = b.dX, a.ldc = h.lddx, a.cmap = row_map(b.slots, h.M, 1), a.cf32 = sizeof(T) == 4;
+        a.rows = h.M, a.N = h.K, a.ka = np, a.kb = h.N, a.splits = p.splits;
+        if ((e = run_product<T, kDx>(a, p.tile, s)) != hipSuccess) return e;
+    }
+    if (b.dW) {
+        a.B = X, a.ldb = ldx, a.gsb = 0, a.bmap = row_map(b.slots, h.M, h.share);
+        a.C = b.dW, a.ldc = h.K, a.gsc = h.N * h.K, a.cf32 = sizeof(T) == 4;
+        a.rows = h.N, a.N = h.K, a.splits = p.splits_w;
+        if ((e = run_product<T, kDw>(a, p.tile_w, s)) != hipSuccess) return e;
+    }
+    return e;
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, void *ws, hipStream_t s) {
+    switch (h.dtype) {
+    case FK_F32: return linear_fwd<float>(h, p, b, (char *)ws, s);
+    case FK_BF16: return linear_fwd<__bf16>(h, p, b, (char *)ws, s);
+    default: return linear_fwd<_Float16>(h, p, b, (char *)ws, s);
+    }
+}
+
+hipError_t launch_linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, void *ws, hipStream_t s) {
+    switch (h.dtype) {
+    case FK_F32: return linear_bwd<float>(h, p, b, (char *)ws, s);
+    case FK_BF16: return linear_bwd<__bf16>(h, p, b, (char *)ws, s);
+    default: return linear_bwd<_Float16>(h, p, b, (char *)ws, s);
+    }
+}
+
+}  // namespace fk

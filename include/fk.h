@@ -69,6 +69,10 @@ extern "C" {
 #endif
 
 #define FK_MAX_K 65536
+#define FK_MAX_WIDTH 1048576     /* longest row of the expert-block operators */
+#define FK_MAX_EXPERTS 1024      /* most experts of fk_route                  */
+#define FK_MAX_ROUTE_K 64        /* most slots a row of fk_route, fk_combine  */
+#define FK_MAX_GROUPS 4096       /* most weight matrices of fk_linear         */
 #define FK_MAX_D 4096
 #define FK_MAX_KNN_K 24          /* largest k of fk_knn          */
 #define FK_MAX_KNN_DB 1073741824 /* most database rows of fk_knn */
@@ -308,6 +312,168 @@ fk_status fk_ivf_build(const float *X, int64_t N, int32_t d, int32_t nlist, int3
 size_t fk_knn_workspace_size(int64_t M, int32_t d, int64_t Ndb, int32_t k, int32_t metric);
 fk_status fk_knn(const float *Q, int64_t M, int32_t d, const float *DB, int64_t Ndb, int32_t k, int32_t metric,
                  int32_t score, int32_t *idx, float *dist, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---- The expert block ------------------------------------------------------
+ *
+ * What a model that routes its rows to experts (by learned logits, or by the
+ * clusters of this library) needs beside the clustering: the rows' layer norm,
+ * the router with its balance loss, the experts' products over the slots that
+ * fk_sort_inverse groups by expert, the weighted sum of a row's expert
+ * outputs, and the gradients of each.  The article names MoE routing as a use
+ * of the clustering (section "Real-time MoE routing").
+ *
+ * A block of T rows, k slots a row and E experts runs
+ *   fk_layer_norm -> fk_linear (router) -> fk_route -> fk_sort_inverse
+ *   (the ids as T k keys of E + 1 clusters) -> fk_linear (grouped, up)
+ *   -> fk_linear (grouped, down) -> fk_combine.
+ *
+ * Common to them: matrices are row-major in FK_F32, FK_BF16 or FK_F16, rows
+ * may be further apart than they are long (the ld arguments, in elements), and
+ * columns are contiguous.  Every sum, softmax, norm and statistic is fp32 and
+ * rounded once to the output's type.  Results are bitwise reproducible (no
+ * floating-point atomics).  Outputs must not overlap inputs, except where said.
+ * Sizes of zero rows are accepted; gradients of parameters are then zero.
+ * NaN and infinities go through by the formulas unless said otherwise.
+ */
+typedef enum { FK_F32 = 0, FK_BF16 = 1, FK_F16 = 2 } fk_dtype;
+
+typedef enum {
+    FK_ACT_NONE = 0,
+    FK_ACT_RELU = 1,
+    FK_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2                          */
+    FK_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2    */
+    FK_ACT_SILU = 4       /* z / (1 + e^-z)                                       */
+} fk_act;
+
+typedef enum {
+    FK_GATES_CHOSEN = 0, /* softmax over the chosen experts (they sum to 1) */
+    FK_GATES_ALL = 1     /* the chosen experts' softmax over all experts    */
+} fk_gates;
+
+/*
+ * Layer norm: Y[i] = (X[i] - mean) rstd weight + bias over each row of d
+ * elements, rstd = 1 / sqrt(mean of the squared deviations + eps).  weight and
+ * bias [d] are of type wdtype (dtype or FK_F32) and may be NULL (1 and 0).
+ * mean and rstd [rows] fp32 may be NULL.  Y may be X itself (same row
+ * stride).  1 <= d <= FK_MAX_WIDTH, eps >= 0.  Device pointers.
+ */
+fk_status fk_layer_norm(int32_t dtype, int32_t wdtype, const void *X, int64_t ldx, int64_t rows, int32_t d,
+                        const void *weight, const void *bias, float eps, void *Y, int64_t ldy, float *mean,
+                        float *rstd, void *stream);
+
+/*
+ * Gradients of fk_layer_norm from dY, with the mean and rstd it wrote: dX, and
+ * dweight and dbias [d] of type wdtype (either may be NULL).  dX may be dY
+ * itself (same row stride) when d <= 8192.  Workspace:
+ * fk_layer_norm_backward_workspace_size() bytes.
+ */
+size_t fk_layer_norm_backward_workspace_size(int64_t rows, int32_t d);
+fk_status fk_layer_norm_backward(int32_t dtype, int32_t wdtype, const void *dY, int64_t lddy, const void *X,
+                                 int64_t ldx, int64_t rows, int32_t d, const float *mean, const float *rstd,
+                                 const void *weight, void *dX, int64_t lddx, void *dweight, void *dbias,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Top-k router over logits[T, E] (row stride ldl): ids[T, k] are the experts of
+ * a row's k largest logits, largest first, the lower index first on ties;
+ * gates[T, k] (fp32) their weights (fk_gates); counts[E] the slots of each
+ * expert; live[1] the rows n that took part; losses[2] (fp32)
+ *   balance = E sum_e (counts[e] / sum counts) (1/n) sum_t softmax(l_t)[e],
+ *   z       = (1/n) sum_t (log sum_e exp l_te)^2.
+ * valid (uint8 [T], may be NULL): rows with 0 are left out, whatever they hold.
+ * A row with nothing above -inf is left out too.  Slots of rows left out, and
+ * slots past a row's last logit above -inf, get id E and gate 0 and are not
+ * counted; with the ids sorted as E + 1 clusters they come last.  A logit of
+ * -inf has probability 0.  NaN is never chosen, but makes the row's
+ * probabilities and so the losses NaN.  k <= E <= FK_MAX_EXPERTS,
+ * k <= FK_MAX_ROUTE_K, T k < 2^31.  Workspace: fk_route_workspace_size().
+ */
+size_t fk_route_workspace_size(int64_t T, int32_t E);
+fk_status fk_route(int32_t dtype, const void *logits, int64_t ldl, int64_t T, int32_t E, int32_t k, int32_t gate_norm,
+                   const uint8_t *valid, int32_t *ids, float *gates, int32_t *counts, float *losses, int32_t *live,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the gates and losses of fk_route with respect to the logits:
+ * d_logits[T, E] (contiguous, the logits' type) from d_gates[T, k] (NULL: 0)
+ * and d_losses[2] (NULL: 0), with the ids, counts and live that fk_route wrote.
+ * The counts are constants (they have no gradient).  Rows left out get 0.
+ */
+fk_status fk_route_backward(int32_t dtype, const void *logits, int64_t ldl, int64_t T, int32_t E, int32_t k,
+                            int32_t gate_norm, const uint8_t *valid, const int32_t *ids, const int32_t *counts,
+                            const int32_t *live, const float *d_gates, const float *d_losses, void *d_logits,
+                            void *stream);
+
+/*
+ * Products with an epilogue, for one weight matrix or one for each group of
+ * rows.
+ *   groups = 0:  Y[i] = act(X[i] W^T + bias) + residual[i],  i < M;
+ *     X[M, K], W[N, K], bias[N], residual and Y [M, N]; slots and offsets NULL.
+ *   groups > 0:  Y[s] = act(X[s / share] W_g^T + bias_g) + residual[s] for the
+ *     slots s = slots[p], offsets[g] <= p < offsets[g + 1]: X[M / share, K],
+ *     W[groups, N, K] (rows ldw apart throughout), bias[groups, N], residual
+ *     and Y [M, N] by slot.  slots[M] is a permutation of 0..M-1 and
+ *     offsets[0..groups] rises from 0, both int32 in device memory
+ *     (fk_sort_inverse writes them); slots NULL stands for slots[p] = p.  The
+ *     rows of slots past offsets[groups] are set to 0.
+ * pre (may be NULL) receives the pre-activations X W^T + bias, of X's type, for
+ * fk_linear_backward.  bias and residual may be NULL; residual may be Y itself
+ * (same row stride and type).  X, W, residual and pre are of type dtype, bias
+ * of bias_dtype (dtype or FK_F32), Y of ydtype (dtype or FK_F32).  X, W, dY
+ * and pre start on 16 bytes; rows of whole 16-byte chunks (K and the row
+ * strides multiples of 8, or of 4 in fp32) are read as they lie, others are
+ * laid out once more in the workspace.  Workspace:
+ * fk_linear_workspace_size(shape, 0).
+ */
+typedef struct {
+    int32_t dtype, ydtype, bias_dtype; /* fk_dtype                                */
+    int32_t act;                       /* fk_act                                  */
+    int32_t groups;                    /* weight matrices by group, 0: one, plain */
+    int32_t share;                     /* consecutive slots that share a row of X */
+    int64_t M, N, K;                   /* rows of Y, columns of Y, columns of X   */
+    int64_t ldx, ldw, ldr, ldy, ldpre; /* row strides of X, W, residual, Y or dY, pre */
+} fk_linear_shape;
+size_t fk_linear_workspace_size(const fk_linear_shape *shape, int32_t backward);
+fk_status fk_linear(const fk_linear_shape *shape, const void *X, const void *W, const void *bias,
+                    const void *residual, const int32_t *slots, const int32_t *offsets, void *Y, void *pre,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of fk_linear from dY (type ydtype, row stride ldy), with the
+ * pre-activations it kept (NULL when act is FK_ACT_NONE): with dZ = dY act'(pre),
+ *   dX[s] = dZ[s] W_g  [M, K] contiguous, a row for each slot (rows that share
+ *     one of X are added by fk_combine without gates),
+ *   dW_g = sum of dZ[s]^T X[s / share]  [groups, N, K] contiguous,
+ *   dbias_g = sum of dZ[s]  [groups, N], of bias_dtype.
+ * Any of them may be NULL.  The residual's gradient is dY itself.  dZ is
+ * rounded to dtype before the products (not for dbias), as the matrix
+ * instructions take it; dX and dW are of type dtype.  Slots past
+ * offsets[groups] get dX 0 and add nothing.  Workspace:
+ * fk_linear_workspace_size(shape, 1).
+ */
+fk_status fk_linear_backward(const fk_linear_shape *shape, const void *dY, const void *X, const void *W,
+                             const void *pre, const int32_t *slots, const int32_t *offsets, void *dX, void *dW,
+                             void *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Weighted sum of the slots of each row: out[t] = residual[t] +
+ * sum_{j<k} gates[t, j] Y[t k + j], in slot order.  Y[rows k, d] is
+ * contiguous; gates[rows, k] fp32 (NULL: all 1); residual (may be NULL) and out
+ * have row strides ldr and ldo, and may be the same matrix (same stride).  A
+ * slot with gate 0 is not read.  k <= FK_MAX_ROUTE_K, d <= FK_MAX_WIDTH.
+ */
+fk_status fk_combine(int32_t dtype, const void *Y, int64_t rows, int32_t k, int32_t d, const float *gates,
+                     const void *residual, int64_t ldr, void *out, int64_t ldo, void *stream);
+
+/*
+ * Gradients of fk_combine from dOut (row stride lddo): dY[t k + j] =
+ * gates[t, j] dOut[t] (0 for a gate of 0) and dgates[t, j] = dOut[t] .
+ * Y[t k + j] (dgates may be NULL; Y is not read then and may be NULL).  The
+ * residual's gradient is dOut itself.
+ */
+fk_status fk_combine_backward(int32_t dtype, const void *dOut, int64_t lddo, const void *Y, int64_t rows, int32_t k,
+                              int32_t d, const float *gates, void *dY, float *dgates, void *stream);
 
 /* Static name of a status code. */
 const char *fk_status_str(int32_t status);
