@@ -495,22 +495,23 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         rows_ahead(kbeg + BK);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        for (int64_t st = 0; st < steps; st += 2) {
-            const int64_t k = kbeg + st * BK;
-            if (st + 1 < steps) {
-                issue(k + BK, sA1, sB1);
-                rows_ahead(k + 2 * BK);
-            }
+        // loads past the end of the sum bring zeros, so the loop needs no
+        // conditions
+        int64_t k = kbeg;
+        for (int64_t st = steps >> 1; st > 0; --st, k += 2 * BK) {
+            issue(k + BK, sA1, sB1);
+            rows_ahead(k + 2 * BK);
             multiply(sA0, sB0);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();
-            if (st + 1 >= steps) break;
-            if (st + 2 < steps) {
-                issue(k + 2 * BK, sA0, sB0);
-                rows_ahead(k + 3 * BK);
-            }
+            issue(k + 2 * BK, sA0, sB0);
+            rows_ahead(k + 3 * BK);
             multiply(sA1, sB1);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+        }
+        if (steps & 1) {
+            multiply(sA0, sB0);
             __syncthreads();
         }
     }
