@@ -208,8 +208,8 @@ struct LinArgs {
 // One operand's tile: ROWS rows (or columns) of C by 128 bytes of the sum, in
 // LDS as 16-byte chunks.
 //   KM (the sum is contiguous in memory): LDS row r holds 8 chunks, chunk c at
-//     place c ^ (r & 7): the 8 lanes that read a chunk of 8 consecutive rows
-//     meet 8 different places.
+//     place c ^ (r >> 1 & 7): 16 lanes that read the same chunk of 16
+//     consecutive rows meet 16 different places of the 64 banks.
 //   otherwise (rows of the operand are steps of the sum): LDS row k holds the
 //     tile's columns, chunk c at place c ^ ((k & 3) << 2): the four rows that a
 //     transposing read takes lie 64 bytes apart.
@@ -218,38 +218,46 @@ struct LinArgs {
 template <typename T, bool KM, int ROWS, int NT>
 struct Operand {
     static constexpr int E = 16 / (int)sizeof(T);       // elements a chunk
+    static constexpr int BK = 8 * E;                    // steps of the sum in a tile
     static constexpr int IT = ROWS * 8 / NT;            // loads a thread
     static constexpr int CPR = KM ? 8 : ROWS / E;       // chunks a LDS row
     static constexpr int STEP = NT / CPR;               // LDS rows a load of all threads covers
-    const T *p[KM ? IT : 1];
-    int kofs;       // KM: this thread's chunk in the 128 bytes; else its row of the sum
-    int64_t ld;
+    const T *p[IT];   // KM and rows without slots: where the next tile's chunks lie
+    int64_t kofs;     // KM: this thread's chunk in the 128 bytes; else its row of the sum
+    int64_t ld, adv;  // adv: elements from one tile to the next
     int32_t idx[KM ? 1 : IT];
     RowMap map;
     int64_t pos0;
+    const T *col;     // not KM: the thread's columns in row 0
 
     // KM: rows [r0, r0 + n) of C at positions; out of range rows repeat the last
-    __device__ __forceinline__ void init_km(const T *base, int64_t ld_, const RowMap &m, int64_t r0, int64_t n) {
+    __device__ __forceinline__ void init_km(const T *base, int64_t ld_, const RowMap &m, int64_t r0, int64_t n,
+                                            int64_t k0) {
         const int row = threadIdx.x >> 3;
-        kofs = ((threadIdx.x & 7) ^ (row & 7)) * E;
+        kofs = ((threadIdx.x & 7) ^ ((row >> 1) & 7)) * E;
+        adv = BK;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int64_t r = row + i * STEP;
-            p[i] = base + m(r0 + (r < n ? r : n - 1)) * ld_ + kofs;
+            p[i] = base + m(r0 + (r < n ? r : n - 1)) * ld_ + kofs + k0;
         }
     }
-    // not KM: columns [c0, cols), the sum over positions from pos
+    // not KM: columns [c0, cols), the sum over positions from pos; out of range
+    // columns repeat the last chunk
     __device__ __forceinline__ void init_mn(const T *base, int64_t ld_, const RowMap &m, int64_t c0, int64_t cols,
-                                            int64_t pos) {
+                                            int64_t pos, int64_t k0) {
         kofs = threadIdx.x / CPR;
         const int64_t c = c0 + (int64_t)((threadIdx.x % CPR) ^ ((kofs & 3) << 2)) * E;
         const int64_t lastc = (cols - 1) / E * E;
-        p[0] = base + (c < lastc ? c : lastc);
+        col = base + (c < lastc ? c : lastc);
         ld = ld_;
+        adv = BK * ld;
         map = m;
         pos0 = pos;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) p[i] = col + (pos + k0 + kofs + i * STEP) * ld;
     }
-    // not KM: the slots of the next tile of the sum
+    // not KM: the slots of the tile at k0 (kend > 0: where the sum ends)
     __device__ __forceinline__ void fetch_rows(int64_t k0, int64_t kend) {
         if constexpr (!KM) {
             if (map.slots != nullptr) {
@@ -261,18 +269,36 @@ struct Operand {
             }
         }
     }
-    __device__ __forceinline__ void issue(int64_t k0, int64_t kend, T *lds, int wave) const {
+    static __device__ __forceinline__ void to_lds(const void *src, T *lds, int i, int wave) {
+        __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(lds + (i * NT + wave * 64) * E), 16, 0, 0);
+    }
+    // The next whole tile; `go`: whether another one follows it (else the same
+    // tile is what the next call loads, into a buffer that is not read).
+    __device__ __forceinline__ void issue(T *lds, int wave, bool go) {
+        const int64_t by = go ? adv : 0;
+        if (!KM && map.slots != nullptr) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) to_lds(col + map.of(idx[i]) * ld, lds, i, wave);
+        } else {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                to_lds(p[i], lds, i, wave);
+                p[i] += by;
+            }
+        }
+    }
+    // The tile at k0 that the sum ends in: zeros past kend.  `after`: whole
+    // tiles came before it (p still points at the last of them).
+    __device__ __forceinline__ void issue_last(int64_t k0, int64_t kend, bool after, T *lds, int wave) {
+        if constexpr (!KM) {
+            fetch_rows(k0, kend);
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const void *src;
-            if constexpr (KM) {
-                src = k0 + kofs < kend ? (const void *)(p[i] + k0) : (const void *)g_zeros;
-            } else {
-                const int64_t k = k0 + kofs + i * STEP;
-                const int64_t r = map.slots != nullptr ? map.of(idx[i]) : pos0 + k;
-                src = k < kend ? (const void *)(p[0] + r * ld) : (const void *)g_zeros;
-            }
-            __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(lds + (i * NT + wave * 64) * E), 16, 0, 0);
+            const int64_t k = KM ? k0 + kofs : k0 + kofs + i * STEP;
+            const T *src = p[i] + (after ? adv : 0);
+            if (!KM && map.slots != nullptr) src = col + map.of(idx[i]) * ld;
+            to_lds(k < kend ? (const void *)src : (const void *)g_zeros, lds, i, wave);
         }
     }
     // The lane's 16 bytes for rows (columns) [r0, r0 + 32) and 32-byte step s
@@ -280,7 +306,7 @@ struct Operand {
         const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
         if constexpr (KM) {
             const int r = r0 + l;
-            return *reinterpret_cast<const typename Mma<T>::Frag *>(lds + (r * 8 + ((s * 2 + h) ^ (r & 7))) * E);
+            return *reinterpret_cast<const typename Mma<T>::Frag *>(lds + (r * 8 + ((s * 2 + h) ^ ((r >> 1) & 7))) * E);
         } else if constexpr (sizeof(T) == 4) {
             typename Mma<T>::Frag f;
 #pragma unroll
@@ -435,8 +461,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
     const int64_t c0 = nt * BN;
     const bool rest = KIND != kDw && a.offsets != nullptr && t.g == a.G;
 
-    // the part of the sum that this split takes
-    const int64_t kall = ka > kb ? ka : kb;
+    // the part of the sum that this split takes: `full` whole tiles from kbeg,
+    // and the one that the sum ends in (`ends`)
+    const int64_t kall = ka > kb ? ka : kb, kmin = ka < kb ? ka : kb;
     int64_t steps = (kall + BK - 1) / BK;
     if (a.splits > 1) {
         const int64_t each = (steps + a.splits - 1) / a.splits;
@@ -445,17 +472,19 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         steps = left < each ? (left > 0 ? left : 0) : each;
     }
     if (rest) steps = 0;
+    const bool ends = steps > 0 && kbeg + steps * BK > kmin;
+    const int64_t full = ends ? steps - 1 : steps;
 
     Operand<T, AKM, BM, NT> oa;
     Operand<T, BKM, BN, NT> ob;
     const T *Bg = (const T *)a.B + (KIND == kDw || rest ? 0 : (int64_t)t.g * a.gsb);
-    if constexpr (AKM) oa.init_km((const T *)a.A, a.lda, a.amap, r0, nrows);
-    else oa.init_mn((const T *)a.A, a.lda, a.amap, r0, a.rows, pos);
+    if constexpr (AKM) oa.init_km((const T *)a.A, a.lda, a.amap, r0, nrows, kbeg);
+    else oa.init_mn((const T *)a.A, a.lda, a.amap, r0, a.rows, pos, kbeg);
     if constexpr (BKM) {
         const RowMap id{nullptr, 0, 0, 0};
-        ob.init_km(Bg, a.ldb, id, c0, a.N - c0 < BN ? a.N - c0 : BN);
+        ob.init_km(Bg, a.ldb, id, c0, a.N - c0 < BN ? a.N - c0 : BN, kbeg);
     } else {
-        ob.init_mn(Bg, a.ldb, a.bmap, c0, a.N, pos);
+        ob.init_mn(Bg, a.ldb, a.bmap, c0, a.N, pos, kbeg);
     }
 
     v16f acc[TM][TN];
@@ -467,54 +496,82 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
-    auto issue = [&](int64_t k0, T *sa, T *sb) {
-        oa.issue(k0, ka, sa, wave);
-        ob.issue(k0, kb, sb, wave);
+    typename Mma<T>::Frag fa[2][TM], fb[2][TN];
+    auto read = [&](const T *sa, const T *sb, int s) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[s & 1][j] = ob.frag(sb, wn + j * 32, s);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[s & 1][i] = oa.frag(sa, wm + i * 32, s);
     };
-    auto rows_ahead = [&](int64_t k0) {
-        oa.fetch_rows(k0, ka);
-        ob.fetch_rows(k0, kb);
+    auto multiply = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::m32(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
     };
-    auto multiply = [&](const T *sa, const T *sb) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            typename Mma<T>::Frag fa[TM], fb[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = ob.frag(sb, wn + j * 32, s);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = oa.frag(sa, wm + i * 32, s);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::m32(fb[j], fa[i], acc[i][j]);
-        }
-    };
-    if (steps > 0) {
-        rows_ahead(kbeg);
-        issue(kbeg, sA0, sB0);
-        rows_ahead(kbeg + BK);
+    auto landed = [&]() {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        // loads past the end of the sum bring zeros, so the loop needs no
-        // conditions
-        int64_t k = kbeg;
-        for (int64_t st = steps >> 1; st > 0; --st, k += 2 * BK) {
-            issue(k + BK, sA1, sB1);
-            rows_ahead(k + 2 * BK);
-            multiply(sA0, sB0);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-            issue(k + 2 * BK, sA0, sB0);
-            rows_ahead(k + 3 * BK);
-            multiply(sA1, sB1);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
+    };
+    // One tile: its first step's operands are in registers on entry, and the
+    // next tile's on return.  Each step's operands are read while the step
+    // before is multiplied, across the tiles' border too: once the last step's
+    // have been read, the other buffer's loads are waited for, and the loads
+    // of the tile after the next go out to this buffer while the last step
+    // and the whole next tile are multiplied.
+    auto tile = [&](T *sa, T *sb, T *na, T *nb, bool go, int64_t ahead) {
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            read(sa, sb, s + 1);
+            multiply(s);
         }
-        if (steps & 1) {
-            multiply(sA0, sB0);
-            __syncthreads();
+        landed();
+        oa.issue(sa, wave, go);
+        ob.issue(sb, wave, go);
+        if constexpr (KIND == kDw) {
+            oa.fetch_rows(ahead, ka);
+            ob.fetch_rows(ahead, kb);
+        }
+        read(na, nb, 0);
+        multiply(3);
+    };
+    if (full > 0) {
+        auto start = [&](T *sa, T *sb, int64_t at) {
+            if constexpr (KIND == kDw) {
+                oa.fetch_rows(kbeg + at * BK, ka);
+                ob.fetch_rows(kbeg + at * BK, kb);
+            }
+            oa.issue(sa, wave, at + 1 < full);
+            ob.issue(sb, wave, at + 1 < full);
+        };
+        start(sA0, sB0, 0);
+        start(sA1, sB1, 1);
+        if constexpr (KIND == kDw) {
+            oa.fetch_rows(kbeg + 2 * BK, ka);
+            ob.fetch_rows(kbeg + 2 * BK, kb);
+        }
+        landed();
+        read(sA0, sB0, 0);
+        int64_t i = 0;
+        for (; i + 2 <= full; i += 2) {
+            tile(sA0, sB0, sA1, sB1, i + 3 < full, kbeg + (i + 3) * BK);
+            tile(sA1, sB1, sA0, sB0, i + 4 < full, kbeg + (i + 4) * BK);
+        }
+        if (i < full) tile(sA0, sB0, sA1, sB1, false, kbeg);
+    }
+    if (ends) {
+        landed();
+        const int64_t k = kbeg + full * BK;
+        oa.issue_last(k, ka, full > 0, sA0, wave);
+        ob.issue_last(k, kb, full > 0, sB0, wave);
+        landed();
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            read(sA0, sB0, s);
+            multiply(s);
         }
     }
+    landed();
 
     // ---- out: 32 rows of 64 columns a wave at a time through LDS, so that the
     // rows leave in whole chunks.  A lane holds one row of C and 4 columns
