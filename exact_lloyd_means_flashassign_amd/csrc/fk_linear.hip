@@ -223,7 +223,7 @@ struct Operand {
     static constexpr int CPR = KM ? 8 : ROWS / E;       // chunks a LDS row
     static constexpr int STEP = NT / CPR;               // LDS rows a load of all threads covers
     const T *p[IT];   // KM and rows without slots: where the next tile's chunks lie
-    int64_t kofs;     // KM: this thread's chunk in the 128 bytes; else its row of the sum
+    int kofs;         // KM: this thread's chunk in the 128 bytes; else its row of the sum
     int64_t ld, adv;  // adv: elements from one tile to the next
     int32_t idx[KM ? 1 : IT];
     RowMap map;
@@ -272,33 +272,14 @@ struct Operand {
     static __device__ __forceinline__ void to_lds(const void *src, T *lds, int i, int wave) {
         __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(lds + (i * NT + wave * 64) * E), 16, 0, 0);
     }
-    // The next whole tile; `go`: whether another one follows it (else the same
-    // tile is what the next call loads, into a buffer that is not read).
-    __device__ __forceinline__ void issue(T *lds, int wave, bool go) {
-        const int64_t by = go ? adv : 0;
-        if (!KM && map.slots != nullptr) {
-#pragma unroll
-            for (int i = 0; i < IT; ++i) to_lds(col + map.of(idx[i]) * ld, lds, i, wave);
-        } else {
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                to_lds(p[i], lds, i, wave);
-                p[i] += by;
-            }
-        }
-    }
-    // The tile at k0 that the sum ends in: zeros past kend.  `after`: whole
-    // tiles came before it (p still points at the last of them).
-    __device__ __forceinline__ void issue_last(int64_t k0, int64_t kend, bool after, T *lds, int wave) {
-        if constexpr (!KM) {
-            fetch_rows(k0, kend);
-        }
+    // The next tile, of which `rem` steps of the sum are left: zeros past them.
+    __device__ __forceinline__ void issue(T *lds, int wave, int rem) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int64_t k = KM ? k0 + kofs : k0 + kofs + i * STEP;
-            const T *src = p[i] + (after ? adv : 0);
-            if (!KM && map.slots != nullptr) src = col + map.of(idx[i]) * ld;
-            to_lds(k < kend ? (const void *)src : (const void *)g_zeros, lds, i, wave);
+            const T *src = !KM && map.slots != nullptr ? col + map.of(idx[i]) * ld : p[i];
+            const int k = KM ? kofs : kofs + i * STEP;
+            to_lds(k < rem ? (const void *)src : (const void *)g_zeros, lds, i, wave);
+            p[i] += adv;
         }
     }
     // The lane's 16 bytes for rows (columns) [r0, r0 + 32) and 32-byte step s
@@ -461,9 +442,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
     const int64_t c0 = nt * BN;
     const bool rest = KIND != kDw && a.offsets != nullptr && t.g == a.G;
 
-    // the part of the sum that this split takes: `full` whole tiles from kbeg,
-    // and the one that the sum ends in (`ends`)
-    const int64_t kall = ka > kb ? ka : kb, kmin = ka < kb ? ka : kb;
+    // the part of the sum that this split takes
+    const int64_t kall = ka > kb ? ka : kb;
     int64_t steps = (kall + BK - 1) / BK;
     if (a.splits > 1) {
         const int64_t each = (steps + a.splits - 1) / a.splits;
@@ -472,8 +452,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         steps = left < each ? (left > 0 ? left : 0) : each;
     }
     if (rest) steps = 0;
-    const bool ends = steps > 0 && kbeg + steps * BK > kmin;
-    const int64_t full = ends ? steps - 1 : steps;
+    // what is left of the sum from tile i on, in A and in B
+    const int64_t kend = kbeg + steps * BK;
+    const int64_t ea = ka < kend ? ka : kend, eb = kb < kend ? kb : kend;
+    auto left = [&](int64_t end, int64_t i) {
+        const int64_t r = end - kbeg - i * BK;
+        return r > BK ? BK : (int)r;
+    };
 
     Operand<T, AKM, BM, NT> oa;
     Operand<T, BKM, BN, NT> ob;
@@ -509,40 +494,59 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::m32(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
     };
+    // The order of a step's instructions: a read (of the next step's operands)
+    // and a product in turn.
+    // `loads` of them also send a load of a later tile on its way.
+    auto spread = [&](int loads) {
+        constexpr int READS = (AKM ? 1 : 16 / (int)sizeof(T) == 4 ? 4 : 2) * TM + (BKM ? 1 : 16 / (int)sizeof(T) == 4 ? 4 : 2) * TN;
+        constexpr int PRODUCTS = TM * TN * (sizeof(T) == 4 ? 4 : 1);
+        constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;
+#pragma unroll
+        for (int i = 0; i < PRODUCTS; ++i) {
+            if (i * EACH < READS) __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+            if (i < loads) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        }
+    };
+    // every load to LDS so far has arrived, in every wave (the builtin, whose
+    // wait the compiler counts, so that it adds none of its own before the
+    // reads: vmcnt(0), the other counters left alone)
     auto landed = [&]() {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
     };
     // One tile: its first step's operands are in registers on entry, and the
     // next tile's on return.  Each step's operands are read while the step
     // before is multiplied, across the tiles' border too: once the last step's
     // have been read, the other buffer's loads are waited for, and the loads
-    // of the tile after the next go out to this buffer while the last step
-    // and the whole next tile are multiplied.
-    auto tile = [&](T *sa, T *sb, T *na, T *nb, bool go, int64_t ahead) {
+    // of the tile after the next (number `ahead`) go out to this buffer while
+    // the last step and the whole next tile are multiplied.
+    auto tile = [&](T *sa, T *sb, T *na, T *nb, int64_t ahead) {
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             read(sa, sb, s + 1);
             multiply(s);
+            spread(0);
         }
         landed();
-        oa.issue(sa, wave, go);
-        ob.issue(sb, wave, go);
+        oa.issue(sa, wave, left(ea, ahead));
+        ob.issue(sb, wave, left(eb, ahead));
         if constexpr (KIND == kDw) {
-            oa.fetch_rows(ahead, ka);
-            ob.fetch_rows(ahead, kb);
+            oa.fetch_rows(kbeg + (ahead + 1) * BK, ka);
+            ob.fetch_rows(kbeg + (ahead + 1) * BK, kb);
         }
         read(na, nb, 0);
         multiply(3);
+        spread(2 * BM * 8 / NT);
     };
-    if (full > 0) {
-        auto start = [&](T *sa, T *sb, int64_t at) {
+    if (steps > 0) {
+        auto start = [&](T *sa, T *sb, int64_t i) {
             if constexpr (KIND == kDw) {
-                oa.fetch_rows(kbeg + at * BK, ka);
-                ob.fetch_rows(kbeg + at * BK, kb);
+                oa.fetch_rows(kbeg + i * BK, ka);
+                ob.fetch_rows(kbeg + i * BK, kb);
             }
-            oa.issue(sa, wave, at + 1 < full);
-            ob.issue(sb, wave, at + 1 < full);
+            oa.issue(sa, wave, left(ea, i));
+            ob.issue(sb, wave, left(eb, i));
         };
         start(sA0, sB0, 0);
         start(sA1, sB1, 1);
@@ -552,23 +556,10 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         }
         landed();
         read(sA0, sB0, 0);
-        int64_t i = 0;
-        for (; i + 2 <= full; i += 2) {
-            tile(sA0, sB0, sA1, sB1, i + 3 < full, kbeg + (i + 3) * BK);
-            tile(sA1, sB1, sA0, sB0, i + 4 < full, kbeg + (i + 4) * BK);
-        }
-        if (i < full) tile(sA0, sB0, sA1, sB1, false, kbeg);
-    }
-    if (ends) {
-        landed();
-        const int64_t k = kbeg + full * BK;
-        oa.issue_last(k, ka, full > 0, sA0, wave);
-        ob.issue_last(k, kb, full > 0, sB0, wave);
-        landed();
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            read(sA0, sB0, s);
-            multiply(s);
+        // two tiles a round; of an odd number the last one's partner is zeros
+        for (int64_t i = 0; i < steps; i += 2) {
+            tile(sA0, sB0, sA1, sB1, i + 2);
+            tile(sA1, sB1, sA0, sB0, i + 3);
         }
     }
     landed();
