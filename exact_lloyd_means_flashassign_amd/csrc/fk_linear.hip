@@ -7,6 +7,8 @@
 // p runs over the positions of a slot list sorted by group: slot(p) =
 // slots[p], row(p) = slots[p] / share, and group g owns [offsets[g],
 // offsets[g+1]).  A plain product has one group and slot(p) = row(p) = p.
+#include <type_traits>
+
 #include "fk.h"
 #include "fk_block.h"
 #include "fk_internal.h"
@@ -205,6 +207,20 @@ struct LinArgs {
     int G, act, splits, skip, cf32, bf32;
 };
 
+// 16 bytes a lane from memory to LDS, lane after lane from `lds` (the same in
+// every lane).  Written in assembly because the compiler, which cannot tell
+// that a transposing read and a load under way touch different tiles, would
+// wait for every load before the next such read; here the caller waits
+// (vmcnt) before it reads what was loaded.  No register is written, and the
+// address is taken when the instruction issues.
+__device__ __forceinline__ void load_to_lds(const void *src, const void *lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is never live across statements
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"((glb_ptr)src), "s"(at) : "m0");
+#pragma clang diagnostic pop
+}
+
 // One operand's tile: ROWS rows (or columns) of C by 128 bytes of the sum, in
 // LDS as 16-byte chunks.
 //   KM (the sum is contiguous in memory): LDS row r holds 8 chunks, chunk c at
@@ -269,18 +285,13 @@ struct Operand {
             }
         }
     }
-    static __device__ __forceinline__ void to_lds(const void *src, T *lds, int i, int wave) {
-        __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(lds + (i * NT + wave * 64) * E), 16, 0, 0);
-    }
-    // The next tile, of which `rem` steps of the sum are left: zeros past them.
-    __device__ __forceinline__ void issue(T *lds, int wave, int rem) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const T *src = !KM && map.slots != nullptr ? col + map.of(idx[i]) * ld : p[i];
-            const int k = KM ? kofs : kofs + i * STEP;
-            to_lds(k < rem ? (const void *)src : (const void *)g_zeros, lds, i, wave);
-            p[i] += adv;
-        }
+    // Load i of the next tile, of which `rem` steps of the sum are left: zeros
+    // past them.
+    __device__ __forceinline__ void issue(const T *lds, int wave, int i, int rem) {
+        const T *src = !KM && map.slots != nullptr ? col + map.of(idx[i]) * ld : p[i];
+        const int k = KM ? kofs : kofs + i * STEP;
+        load_to_lds(k < rem ? (const void *)src : (const void *)g_zeros, lds + (i * NT + wave * 64) * E);
+        p[i] += adv;
     }
     // The lane's 16 bytes for rows (columns) [r0, r0 + 32) and 32-byte step s
     __device__ __forceinline__ static typename Mma<T>::Frag frag(const T *lds, int r0, int s) {
@@ -482,30 +493,29 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
 
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
     typename Mma<T>::Frag fa[2][TM], fb[2][TN];
-    auto read = [&](const T *sa, const T *sb, int s) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) fb[s & 1][j] = ob.frag(sb, wn + j * 32, s);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[s & 1][i] = oa.frag(sa, wm + i * 32, s);
+    // One operand block of step s, number n of TN + TM.
+    auto read = [&](const T *sa, const T *sb, int s, int n) {
+        if (n < TN) fb[s & 1][n] = ob.frag(sb, wn + n * 32, s);
+        else fa[s & 1][n - TN] = oa.frag(sa, wm + (n - TN) * 32, s);
     };
-    auto multiply = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::m32(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
-    };
-    // The order of a step's instructions: a read (of the next step's operands)
-    // and a product in turn.
-    // `loads` of them also send a load of a later tile on its way.
-    auto spread = [&](int loads) {
-        constexpr int READS = (AKM ? 1 : 16 / (int)sizeof(T) == 4 ? 4 : 2) * TM + (BKM ? 1 : 16 / (int)sizeof(T) == 4 ? 4 : 2) * TN;
-        constexpr int PRODUCTS = TM * TN * (sizeof(T) == 4 ? 4 : 1);
-        constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;
+    // The products of step s, with the reads of step r (from ra, rb) and the
+    // loads of a later tile (to la, lb; none without LOADS) spread between
+    // them in this order: each product keeps the matrix unit busy while the
+    // next read or load is sent.
+    constexpr int PRODUCTS = TM * TN, READS = TM + TN, IT = BM * 8 / NT;
+    auto step = [&](int s, const T *ra, const T *rb, int r, auto loads, const T *la, const T *lb, int rem_a, int rem_b) {
+        constexpr int LOADS = decltype(loads)::value;
 #pragma unroll
         for (int i = 0; i < PRODUCTS; ++i) {
-            if (i * EACH < READS) __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
-            if (i < loads) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+#pragma unroll
+            for (int n = i * LOADS / PRODUCTS; n < (i + 1) * LOADS / PRODUCTS; ++n) {
+                if (n < IT) oa.issue(la, wave, n, rem_a);
+                else ob.issue(lb, wave, n - IT, rem_b);
+            }
+#pragma unroll
+            for (int n = i * READS / PRODUCTS; n < (i + 1) * READS / PRODUCTS; ++n) read(ra, rb, r, n);
+            acc[i / TN][i % TN] = Mma<T>::m32(fb[s & 1][i % TN], fa[s & 1][i / TN], acc[i / TN][i % TN]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
     // every load to LDS so far has arrived, in every wave (the builtin, whose
@@ -521,23 +531,18 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
     // have been read, the other buffer's loads are waited for, and the loads
     // of the tile after the next (number `ahead`) go out to this buffer while
     // the last step and the whole next tile are multiplied.
-    auto tile = [&](T *sa, T *sb, T *na, T *nb, int64_t ahead) {
-#pragma unroll
-        for (int s = 0; s < 3; ++s) {
-            read(sa, sb, s + 1);
-            multiply(s);
-            spread(0);
-        }
+    auto tile = [&](const T *sa, const T *sb, const T *na, const T *nb, int64_t ahead) {
+        constexpr std::integral_constant<int, 0> none{};
+        constexpr std::integral_constant<int, 2 * IT> both{};
+        step(0, sa, sb, 1, none, sa, sb, 0, 0);
+        step(1, sa, sb, 2, none, sa, sb, 0, 0);
+        step(2, sa, sb, 3, none, sa, sb, 0, 0);
         landed();
-        oa.issue(sa, wave, left(ea, ahead));
-        ob.issue(sb, wave, left(eb, ahead));
+        step(3, na, nb, 0, both, sa, sb, left(ea, ahead), left(eb, ahead));
         if constexpr (KIND == kDw) {
             oa.fetch_rows(kbeg + (ahead + 1) * BK, ka);
             ob.fetch_rows(kbeg + (ahead + 1) * BK, kb);
         }
-        read(na, nb, 0);
-        multiply(3);
-        spread(2 * BM * 8 / NT);
     };
     if (steps > 0) {
         auto start = [&](T *sa, T *sb, int64_t i) {
@@ -545,8 +550,11 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
                 oa.fetch_rows(kbeg + i * BK, ka);
                 ob.fetch_rows(kbeg + i * BK, kb);
             }
-            oa.issue(sa, wave, left(ea, i));
-            ob.issue(sb, wave, left(eb, i));
+#pragma unroll
+            for (int n = 0; n < IT; ++n) {
+                oa.issue(sa, wave, n, left(ea, i));
+                ob.issue(sb, wave, n, left(eb, i));
+            }
         };
         start(sA0, sB0, 0);
         start(sA1, sB1, 1);
@@ -555,7 +563,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
             ob.fetch_rows(kbeg + 2 * BK, kb);
         }
         landed();
-        read(sA0, sB0, 0);
+#pragma unroll
+        for (int n = 0; n < READS; ++n) read(sA0, sB0, 0, n);
         // two tiles a round; of an odd number the last one's partner is zeros
         for (int64_t i = 0; i < steps; i += 2) {
             tile(sA0, sB0, sA1, sB1, i + 2);
