@@ -213,38 +213,47 @@ struct LinArgs {
 // wait for every load before the next such read; here the caller waits
 // (vmcnt) before it reads what was loaded.  No register is written, and the
 // address is taken when the instruction issues.
-__device__ __forceinline__ void load_to_lds(const void *src, const void *lds) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
+__device__ __forceinline__ void load_to_lds(const void *src, const __attribute__((address_space(3))) void *lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is never live across statements
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"((glb_ptr)src), "s"(at) : "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"((glb_ptr)src), "s"(at) : "m0");
 #pragma clang diagnostic pop
 }
 
-// One operand's tile: ROWS rows (or columns) of C by 128 bytes of the sum, in
-// LDS as 16-byte chunks.
+// One operand's tile: ROWS rows (or columns) of C by 128 bytes of the sum, as
+// two parts of ROWS / 2 rows (columns) in LDS, each of 16-byte chunks.
 //   KM (the sum is contiguous in memory): LDS row r holds 8 chunks, chunk c at
 //     place c ^ (r >> 1 & 7): 16 lanes that read the same chunk of 16
 //     consecutive rows meet 16 different places of the 64 banks.
 //   otherwise (rows of the operand are steps of the sum): LDS row k holds the
-//     tile's columns, chunk c at place c ^ ((k & 3) << 2): the four rows that a
-//     transposing read takes lie 64 bytes apart.
+//     part's columns, chunk c at place c ^ mn_turn(k): the four rows that a
+//     transposing read takes lie on different banks.
 // Loads go from memory straight to LDS, 16 bytes a lane, each lane fetching
-// the chunk that belongs at its place.
+// the chunk that belongs at its place; 8 lanes take the whole 128 bytes of a
+// row, so that every request to L2 is a full line (64-byte rows, which would
+// let LDS hold more steps, took twice the requests and 1.3 times the time).
 template <typename T, bool KM, int ROWS, int NT>
 struct Operand {
+    typedef const __attribute__((address_space(3))) T *Lds;
     static constexpr int E = 16 / (int)sizeof(T);       // elements a chunk
     static constexpr int BK = 8 * E;                    // steps of the sum in a tile
-    static constexpr int IT = ROWS * 8 / NT;            // loads a thread
-    static constexpr int CPR = KM ? 8 : ROWS / E;       // chunks a LDS row
+    static constexpr int PR = ROWS / 2;                 // rows (columns) of a part
+    static constexpr int PART = PR * BK;                // elements of a part
+    static constexpr int IT = PR * 8 / NT;              // loads a thread for a part
+    static constexpr int CPR = KM ? 8 : PR / E;         // chunks a LDS row
     static constexpr int STEP = NT / CPR;               // LDS rows a load of all threads covers
-    const T *p[IT];   // KM and rows without slots: where the next tile's chunks lie
+    static constexpr int RPW = 64 / CPR;                // LDS rows a load of one wave covers
+    const T *p[KM ? 2 * IT : IT];  // where the next tile's chunks lie
     int kofs;         // KM: this thread's chunk in the 128 bytes; else its row of the sum
+    int over;         // not KM: from the first part's columns to the second's
     int64_t ld, adv;  // adv: elements from one tile to the next
     int32_t idx[KM ? 1 : IT];
     RowMap map;
     int64_t pos0;
     const T *col;     // not KM: the thread's columns in row 0
+
+    static __device__ __forceinline__ int mn_turn(int k) { return CPR >= 16 ? (k & 3) << 2 : ((k >> 1) & 1) << 2; }
 
     // KM: rows [r0, r0 + n) of C at positions; out of range rows repeat the last
     __device__ __forceinline__ void init_km(const T *base, int64_t ld_, const RowMap &m, int64_t r0, int64_t n,
@@ -253,7 +262,7 @@ struct Operand {
         kofs = ((threadIdx.x & 7) ^ ((row >> 1) & 7)) * E;
         adv = BK;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
+        for (int i = 0; i < 2 * IT; ++i) {
             const int64_t r = row + i * STEP;
             p[i] = base + m(r0 + (r < n ? r : n - 1)) * ld_ + kofs + k0;
         }
@@ -263,9 +272,11 @@ struct Operand {
     __device__ __forceinline__ void init_mn(const T *base, int64_t ld_, const RowMap &m, int64_t c0, int64_t cols,
                                             int64_t pos, int64_t k0) {
         kofs = threadIdx.x / CPR;
-        const int64_t c = c0 + (int64_t)((threadIdx.x % CPR) ^ ((kofs & 3) << 2)) * E;
+        const int64_t c = c0 + (int64_t)((threadIdx.x % CPR) ^ mn_turn(kofs)) * E;
         const int64_t lastc = (cols - 1) / E * E;
-        col = base + (c < lastc ? c : lastc);
+        const int64_t first = c < lastc ? c : lastc, second = c + PR < lastc ? c + PR : lastc;
+        col = base + first;
+        over = (int)(second - first);
         ld = ld_;
         adv = BK * ld;
         map = m;
@@ -273,38 +284,51 @@ struct Operand {
 #pragma unroll
         for (int i = 0; i < IT; ++i) p[i] = col + (pos + k0 + kofs + i * STEP) * ld;
     }
-    // not KM: the slots of the tile at k0 (kend > 0: where the sum ends)
-    __device__ __forceinline__ void fetch_rows(int64_t k0, int64_t kend) {
+    // not KM: the slots of the tile at k0 (kend > 0: where the sum ends).  They
+    // are read as scalars, a wave's few rows at a time: a vector load would
+    // have to be waited for behind all loads to LDS under way.
+    __device__ __forceinline__ void fetch_rows(int64_t k0, int64_t kend, int wave) {
         if constexpr (!KM) {
             if (map.slots != nullptr) {
+                typedef const __attribute__((address_space(4))) int32_t *const_ptr;
+                const const_ptr s = (const_ptr)(uintptr_t)(map.slots + pos0);
+                const int mine = (threadIdx.x & 63) / CPR;
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
-                    const int64_t k = k0 + kofs + i * STEP;
-                    idx[i] = map.slots[pos0 + (k < kend ? k : kend - 1)];
+#pragma unroll
+                    for (int j = 0; j < RPW; ++j) {
+                        const int64_t k = k0 + wave * RPW + i * STEP + j;
+                        const int32_t v = s[k < kend ? k : kend - 1];
+                        idx[i] = j == 0 || mine == j ? v : idx[i];
+                    }
                 }
             }
         }
     }
-    // Load i of the next tile, of which `rem` steps of the sum are left: zeros
-    // past them.
-    __device__ __forceinline__ void issue(const T *lds, int wave, int i, int rem) {
-        const T *src = !KM && map.slots != nullptr ? col + map.of(idx[i]) * ld : p[i];
+    // Load i of a part of the next tile, of which `rem` steps of the sum are
+    // left: zeros past them.  The second part's loads follow the first's.
+    __device__ __forceinline__ void issue(Lds part, int wave, int half, int i, int rem) {
+        const int n = KM ? half * IT + i : i;
+        const T *src = !KM && map.slots != nullptr ? col + map.of(idx[i]) * ld : p[n];
+        if (!KM && half == 1) src += over;
         const int k = KM ? kofs : kofs + i * STEP;
-        load_to_lds(k < rem ? (const void *)src : (const void *)g_zeros, lds + (i * NT + wave * 64) * E);
-        p[i] += adv;
+        load_to_lds(k < rem ? (const void *)src : (const void *)g_zeros, part + (i * NT + wave * 64) * E);
+        if (KM || half == 1) p[n] += adv;
     }
-    // The lane's 16 bytes for rows (columns) [r0, r0 + 32) and 32-byte step s
-    __device__ __forceinline__ static typename Mma<T>::Frag frag(const T *lds, int r0, int s) {
+    // The lane's 16 bytes for rows (columns) [r0, r0 + 32) of a part and
+    // 32-byte step s
+    __device__ __forceinline__ static typename Mma<T>::Frag frag(Lds lds, int r0, int s) {
         const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
         if constexpr (KM) {
             const int r = r0 + l;
-            return *reinterpret_cast<const typename Mma<T>::Frag *>(lds + (r * 8 + ((s * 2 + h) ^ ((r >> 1) & 7))) * E);
+            typedef const __attribute__((address_space(3))) typename Mma<T>::Frag *P;
+            return *(P)(lds + (r * 8 + ((s * 2 + h) ^ ((r >> 1) & 7))) * E);
         } else if constexpr (sizeof(T) == 4) {
             typename Mma<T>::Frag f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int k = s * 8 + h * 4 + i, c = r0 + l;
-                f[i] = lds[k * ROWS + ((c / E) ^ ((k & 3) << 2)) * E + c % E];
+                f[i] = lds[k * PR + ((c / E) ^ mn_turn(k)) * E + c % E];
             }
             return f;
         } else {
@@ -312,10 +336,10 @@ struct Operand {
             // (4 steps of the sum) each
             const int i = lane & 15, c = r0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
             const int k = s * 16 + h * 8 + (i >> 2);
-            const T *q = lds + k * ROWS + ((c / E) ^ ((k & 3) << 2)) * E + c % E;
+            const Lds q = lds + k * PR + ((c / E) ^ mn_turn(k)) * E + c % E;
             typedef __attribute__((address_space(3))) v4s *P;
             const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q);
-            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * ROWS));
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * PR));
             const v8s both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             return __builtin_bit_cast(typename Mma<T>::Frag, both);
         }
@@ -392,21 +416,35 @@ struct Epilogue {
     }
 };
 
-// BM x BN of C a workgroup of WM x WN waves, 128 bytes of the sum a step, two
-// tiles of each operand in LDS: one is multiplied while the next one's loads
-// are in flight.
-template <typename T, int KIND, int BM, int BN, int WM, int WN>
+// BS x BS of C a workgroup of WM x WN waves, the sum in tiles of 128 bytes of
+// each row, two tiles of both operands in LDS.
+//
+// Each operand's tile lies in two parts, and a wave's block of C takes rows
+// from both parts of A and columns from both parts of B.  A wave goes through
+// a tile in two turns: it reads A's first part and both of B's and multiplies
+// them, then reads A's second part and multiplies that.  A part's place in LDS
+// is refilled, with the tile after the next, as soon as every wave has it in
+// registers, so loads have more than a tile's time to arrive.  Reading and
+// multiplying alternate, with a barrier after each; of two waves on a SIMD one
+// reads while the other multiplies.
+template <typename T, int KIND, int BS, int WM, int WN>
 __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtiles, int64_t ntiles) {
     constexpr int NT = WM * WN * 64;
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int BK = 8 * E;
-    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-    static_assert(BN / WN == 64, "the epilogue stages 64 columns a wave");
+    constexpr int BM = BS, BN = BS;
+    constexpr int TA = BM / 2 / WM / 32;  // 32-row blocks of a part that a wave takes
+    static_assert(BN / 2 / WN == 32 && TA >= 1, "a wave takes 32 columns of either part of B");
     constexpr bool AKM = KIND != kDw, BKM = KIND == kFwd;
-    __shared__ __attribute__((aligned(16))) T sA0[BM * BK];
-    __shared__ __attribute__((aligned(16))) T sA1[BM * BK];
-    __shared__ __attribute__((aligned(16))) T sB0[BN * BK];
-    __shared__ __attribute__((aligned(16))) T sB1[BN * BK];
+    typedef Operand<T, AKM, BM, NT> OpA;
+    typedef Operand<T, BKM, BN, NT> OpB;
+    constexpr int PART = OpA::PART;
+    static_assert(OpA::PART == OpB::PART && OpA::IT == 2 && OpB::IT == 2, "parts of one size, two loads a thread each");
+    constexpr bool PING = NT == 512;  // two waves a SIMD: half a turn apart
+    // tile t: parts A0, A1, B0, B1 at (t & 1) * 4
+    __shared__ __attribute__((aligned(256))) T smem[8 * PART];
+    typedef const __attribute__((address_space(3))) T *Lds;
+    const Lds parts = (Lds)smem;
 
     // ---- which tile ----
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -453,7 +491,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
     const int64_t c0 = nt * BN;
     const bool rest = KIND != kDw && a.offsets != nullptr && t.g == a.G;
 
-    // the part of the sum that this split takes
+    // the part of the sum that this split takes, in tiles
     const int64_t kall = ka > kb ? ka : kb;
     int64_t steps = (kall + BK - 1) / BK;
     if (a.splits > 1) {
@@ -471,8 +509,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         return r > BK ? BK : (int)r;
     };
 
-    Operand<T, AKM, BM, NT> oa;
-    Operand<T, BKM, BN, NT> ob;
+    OpA oa;
+    OpB ob;
     const T *Bg = (const T *)a.B + (KIND == kDw || rest ? 0 : (int64_t)t.g * a.gsb);
     if constexpr (AKM) oa.init_km((const T *)a.A, a.lda, a.amap, r0, nrows, kbeg);
     else oa.init_mn((const T *)a.A, a.lda, a.amap, r0, a.rows, pos, kbeg);
@@ -483,108 +521,113 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         ob.init_mn(Bg, a.ldb, a.bmap, c0, a.N, pos, kbeg);
     }
 
-    v16f acc[TM][TN];
+    // acc[i][j]: row block i of A's first part (i < TA) or second, column
+    // block j of B's parts
+    v16f acc[2 * TA][2];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < 2 * TA; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
-    typename Mma<T>::Frag fa[2][TM], fb[2][TN];
-    // One operand block of step s, number n of TN + TM.
-    auto read = [&](const T *sa, const T *sb, int s, int n) {
-        if (n < TN) fb[s & 1][n] = ob.frag(sb, wn + n * 32, s);
-        else fa[s & 1][n - TN] = oa.frag(sa, wm + (n - TN) * 32, s);
+    const int wm = wave / WN * (TA * 32), wn = wave % WN * 32;
+    typename Mma<T>::Frag fa[4][TA], fb[4][2];
+    auto read_a = [&](Lds part) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < TA; ++i) fa[s][i] = OpA::frag(part, wm + i * 32, s);
     };
-    // The products of step s, with the reads of step r (from ra, rb) and the
-    // loads of a later tile (to la, lb; none without LOADS) spread between
-    // them in this order: each product keeps the matrix unit busy while the
-    // next read or load is sent.
-    constexpr int PRODUCTS = TM * TN, READS = TM + TN, IT = BM * 8 / NT;
-    auto step = [&](int s, const T *ra, const T *rb, int r, auto loads, const T *la, const T *lb, int rem_a, int rem_b) {
-        constexpr int LOADS = decltype(loads)::value;
+    auto read_b = [&](Lds part) {
 #pragma unroll
-        for (int i = 0; i < PRODUCTS; ++i) {
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int n = i * LOADS / PRODUCTS; n < (i + 1) * LOADS / PRODUCTS; ++n) {
-                if (n < IT) oa.issue(la, wave, n, rem_a);
-                else ob.issue(lb, wave, n - IT, rem_b);
-            }
-#pragma unroll
-            for (int n = i * READS / PRODUCTS; n < (i + 1) * READS / PRODUCTS; ++n) read(ra, rb, r, n);
-            acc[i / TN][i % TN] = Mma<T>::m32(fb[s & 1][i % TN], fa[s & 1][i / TN], acc[i / TN][i % TN]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int j = 0; j < 2; ++j) fb[s][j] = OpB::frag(part + j * PART, wn, s);
     };
-    // every load to LDS so far has arrived, in every wave (the builtin, whose
-    // wait the compiler counts, so that it adds none of its own before the
-    // reads: vmcnt(0), the other counters left alone)
-    auto landed = [&]() {
-        __builtin_amdgcn_s_waitcnt(0x0F70);
+    // The end of a reading turn: this wave's reads are in registers (the
+    // compiler's own wait, before the barrier), and of its loads to LDS all but
+    // the latest `later` have arrived (vmcnt, which counts them in order; the
+    // other counters are left alone).
+    auto landed = [&](auto later) {
+        constexpr int n = decltype(later)::value;
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
         __syncthreads();
     };
-    // One tile: its first step's operands are in registers on entry, and the
-    // next tile's on return.  Each step's operands are read while the step
-    // before is multiplied, across the tiles' border too: once the last step's
-    // have been read, the other buffer's loads are waited for, and the loads
-    // of the tile after the next (number `ahead`) go out to this buffer while
-    // the last step and the whole next tile are multiplied.
-    auto tile = [&](const T *sa, const T *sb, const T *na, const T *nb, int64_t ahead) {
-        constexpr std::integral_constant<int, 0> none{};
-        constexpr std::integral_constant<int, 2 * IT> both{};
-        step(0, sa, sb, 1, none, sa, sb, 0, 0);
-        step(1, sa, sb, 2, none, sa, sb, 0, 0);
-        step(2, sa, sb, 3, none, sa, sb, 0, 0);
-        landed();
-        step(3, na, nb, 0, both, sa, sb, left(ea, ahead), left(eb, ahead));
+    auto rows_of = [&](int64_t i) {
         if constexpr (KIND == kDw) {
-            oa.fetch_rows(kbeg + (ahead + 1) * BK, ka);
-            ob.fetch_rows(kbeg + (ahead + 1) * BK, kb);
+            oa.fetch_rows(kbeg + i * BK, ka, wave);
+            ob.fetch_rows(kbeg + i * BK, kb, wave);
         }
     };
+    // A multiplying turn on A's first or second part, with `loads` loads of a
+    // later tile spread between the products: the matrix unit stays busy while
+    // they are sent.
+    auto multiply = [&](auto second, auto loads, auto load) {
+        constexpr int I0 = decltype(second)::value * TA, LOADS = decltype(loads)::value;
+        constexpr int PRODUCTS = 4 * TA * 2;
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int n = 0; n < PRODUCTS; ++n) {
+            const int s = n / (2 * TA), i = n / 2 % TA, j = n % 2;
+            acc[I0 + i][j] = Mma<T>::m32(fb[s][j], fa[s][i], acc[I0 + i][j]);
+#pragma unroll
+            for (int l = n * LOADS / PRODUCTS; l < (n + 1) * LOADS / PRODUCTS; ++l) load(l);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        if (PING) __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    std::integral_constant<int, 0> none;
+    std::integral_constant<int, 1> one;
+    std::integral_constant<int, 2> two;
+    std::integral_constant<int, 6> six;
     if (steps > 0) {
-        auto start = [&](T *sa, T *sb, int64_t i) {
-            if constexpr (KIND == kDw) {
-                oa.fetch_rows(kbeg + i * BK, ka);
-                ob.fetch_rows(kbeg + i * BK, kb);
-            }
-#pragma unroll
-            for (int n = 0; n < IT; ++n) {
-                oa.issue(sa, wave, n, left(ea, i));
-                ob.issue(sb, wave, n, left(eb, i));
-            }
+        // A's first part and B's parts of a tile (6 loads), and A's second (2)
+        auto most = [&](Lds tile, int l, int ra, int rb) {
+            if (l < 2) oa.issue(tile, wave, 0, l, ra);
+            else ob.issue(tile + (l < 4 ? 2 : 3) * PART, wave, l < 4 ? 0 : 1, l & 1, rb);
         };
-        start(sA0, sB0, 0);
-        start(sA1, sB1, 1);
-        if constexpr (KIND == kDw) {
-            oa.fetch_rows(kbeg + 2 * BK, ka);
-            ob.fetch_rows(kbeg + 2 * BK, kb);
-        }
-        landed();
+        rows_of(0);
 #pragma unroll
-        for (int n = 0; n < READS; ++n) read(sA0, sB0, 0, n);
-        // two tiles a round; of an odd number the last one's partner is zeros
-        for (int64_t i = 0; i < steps; i += 2) {
-            tile(sA0, sB0, sA1, sB1, i + 2);
-            tile(sA1, sB1, sA0, sB0, i + 3);
+        for (int l = 0; l < 6; ++l) most(parts, l, left(ea, 0), left(eb, 0));
+#pragma unroll
+        for (int l = 0; l < 2; ++l) oa.issue(parts + PART, wave, 1, l, left(ea, 0));
+        rows_of(1);
+#pragma unroll
+        for (int l = 0; l < 6; ++l) most(parts + 4 * PART, l, left(ea, 1), left(eb, 1));
+        landed(std::integral_constant<int, 8>{});
+        const bool second = PING && wave >= NT / 128;
+        if (second) __builtin_amdgcn_s_barrier();
+        for (int64_t i = 0; i < steps; ++i) {
+            const Lds tile = parts + (i & 1) * 4 * PART, next = parts + (~i & 1) * 4 * PART;
+            read_a(tile);
+            read_b(tile + 2 * PART);
+            landed(six);  // A's second part of this tile is there
+            const int r1 = left(ea, i + 1);
+            multiply(none, two, [&](int l) { oa.issue(next + PART, wave, 1, l, r1); });
+            rows_of(i + 2);
+            read_a(tile + PART);
+            landed(two);  // the next tile's first part of A and both of B are there
+            const int ra = left(ea, i + 2), rb = left(eb, i + 2);
+            multiply(one, six, [&](int l) { most(tile, l, ra, rb); });
         }
+        if (PING && !second) __builtin_amdgcn_s_barrier();
     }
-    landed();
+    landed(none);
 
     // ---- out: 32 rows of 64 columns a wave at a time through LDS, so that the
     // rows leave in whole chunks.  A lane holds one row of C and 4 columns
     // apiece of it (the operands are multiplied the other way round).
     constexpr int LDS_ROW = 68;
-    constexpr int PER = NT / 256;  // waves that stage in one of the four tiles
-    static_assert(PER * 32 * LDS_ROW * 4 <= BM * 128 && BM == BN, "the staged rows fit the tiles");
-    const int at = wave / PER;
-    float *stage = reinterpret_cast<float *>(at == 0 ? sA0 : at == 1 ? sA1 : at == 2 ? sB0 : sB1) +
-                   wave % PER * 32 * LDS_ROW;
+    static_assert(WM * WN * 32 * LDS_ROW * 4 <= sizeof(smem), "the staged rows fit the tiles");
+    float *stage = reinterpret_cast<float *>(smem) + wave * 32 * LDS_ROW;
     const int lane = threadIdx.x & 63;
     Epilogue<T> ep;
-    const int64_t col = c0 + wn + (lane & 7) * 8;
+    // lanes 0..3 of eight: the wave's columns in B's first part, 4..7: second
+    const int64_t col = c0 + ((lane >> 2) & 1) * (BN / 2) + wn + (lane & 3) * 8;
     if (a.splits > 1 || rest) {
         ep.col = col;
         const int64_t left = a.N - col;
@@ -593,9 +636,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         ep.init(a, t.g, col);
     }
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    for (int i = 0; i < 2 * TA; ++i) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 v4f v;
@@ -609,7 +652,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
             const int row = q * 8 + (lane >> 3);
-            const int64_t r = wm + i * 32 + row;
+            const int64_t r = i / TA * (BM / 2) + wm + i % TA * 32 + row;
             float v[8];
             const v4f lo = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + (lane & 7) * 8);
             const v4f hi = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + (lane & 7) * 8 + 4);
@@ -922,8 +965,8 @@ hipError_t run_product(const LinArgs &a, int tile, hipStream_t s) {
     if (grid > 0) {
         if (grid > INT32_MAX) return hipErrorInvalidValue;
         const dim3 gr((unsigned)grid, (unsigned)a.splits);
-        if (tile == 256) k_product<T, KIND, 256, 256, 2, 4><<<gr, 512, 0, s>>>(a, mt, nt);
-        else k_product<T, KIND, 128, 128, 2, 2><<<gr, 256, 0, s>>>(a, mt, nt);
+        if (tile == 256) k_product<T, KIND, 256, 2, 4><<<gr, 512, 0, s>>>(a, mt, nt);
+        else k_product<T, KIND, 128, 2, 2><<<gr, 256, 0, s>>>(a, mt, nt);
     }
     if (a.splits > 1) {
         const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
