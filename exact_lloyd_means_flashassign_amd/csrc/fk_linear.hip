@@ -134,6 +134,13 @@ __device__ __forceinline__ int64_t group_at(const int32_t *offsets, int g, int64
     return o < 0 ? 0 : ((int64_t)o < M ? (int64_t)o : M);
 }
 
+// a value that is the same in every lane, as a scalar
+__device__ __forceinline__ int64_t scalar(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Finds row tile `want` among the groups' tiles of `rows` rows (groups of
 // `skip` rows or fewer have none).  Group G stands for the positions past the
 // last group (with_rest).  Every lane of a wave calls it and gets the same
@@ -207,22 +214,37 @@ struct LinArgs {
     int G, act, splits, skip, cf32, bf32;
 };
 
+typedef const __attribute__((address_space(3))) void *lds_at;
+
 // 16 bytes a lane from memory to LDS, lane after lane from `lds` (the same in
 // every lane).  Written in assembly because the compiler, which cannot tell
 // that a transposing read and a load under way touch different tiles, would
 // wait for every load before the next such read; here the caller waits
 // (vmcnt) before it reads what was loaded.  No register is written, and the
-// address is taken when the instruction issues.
-__device__ __forceinline__ void load_to_lds(const void *src, const __attribute__((address_space(3))) void *lds) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+// address is taken when the instruction issues.  m0, which holds the place in
+// LDS, needs a wait state before the load.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is never live across statements
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"((glb_ptr)src), "s"(at) : "m0");
-#pragma clang diagnostic pop
+// from a scalar base and a lane's offset in bytes (no address arithmetic in
+// the lanes: 1251 TFLOP/s where lane addresses gave 1210, 16384 x 8192 x 4096)
+__device__ __forceinline__ void load_to_lds(const void *base, uint32_t off, lds_at lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(off), "s"(at),
+                 "s"((glb_ptr)base)
+                 : "m0");
 }
+// from a lane's address
+__device__ __forceinline__ void load_to_lds(const void *src, lds_at lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"((glb_ptr)src), "s"(at)
+                 : "m0");
+}
+#pragma clang diagnostic pop
 
-// One operand's tile: ROWS rows (or columns) of C by 128 bytes of the sum, as
-// two parts of ROWS / 2 rows (columns) in LDS, each of 16-byte chunks.
+constexpr int kTileThreads = 256;  // 4 waves, one a SIMD
+
+// One operand's tile: BS rows (or columns) of C by 128 bytes of the sum, as
+// two parts of BS / 2 rows (columns) in LDS, each of 16-byte chunks.
 //   KM (the sum is contiguous in memory): LDS row r holds 8 chunks, chunk c at
 //     place c ^ (r >> 1 & 7): 16 lanes that read the same chunk of 16
 //     consecutive rows meet 16 different places of the 64 banks.
@@ -231,89 +253,101 @@ __device__ __forceinline__ void load_to_lds(const void *src, const __attribute__
 //     transposing read takes lie on different banks.
 // Loads go from memory straight to LDS, 16 bytes a lane, each lane fetching
 // the chunk that belongs at its place; 8 lanes take the whole 128 bytes of a
-// row, so that every request to L2 is a full line (64-byte rows, which would
-// let LDS hold more steps, took twice the requests and 1.3 times the time).
-template <typename T, bool KM, int ROWS, int NT>
+// row, so that every request to L2 is a full line.
+template <typename T, bool KM, int BS>
 struct Operand {
     typedef const __attribute__((address_space(3))) T *Lds;
+    static constexpr int NT = kTileThreads;
     static constexpr int E = 16 / (int)sizeof(T);       // elements a chunk
     static constexpr int BK = 8 * E;                    // steps of the sum in a tile
-    static constexpr int PR = ROWS / 2;                 // rows (columns) of a part
+    static constexpr int PR = BS / 2;                   // rows (columns) of a part
     static constexpr int PART = PR * BK;                // elements of a part
     static constexpr int IT = PR * 8 / NT;              // loads a thread for a part
     static constexpr int CPR = KM ? 8 : PR / E;         // chunks a LDS row
     static constexpr int STEP = NT / CPR;               // LDS rows a load of all threads covers
     static constexpr int RPW = 64 / CPR;                // LDS rows a load of one wave covers
-    const T *p[KM ? 2 * IT : IT];  // where the next tile's chunks lie
-    int kofs;         // KM: this thread's chunk in the 128 bytes; else its row of the sum
-    int over;         // not KM: from the first part's columns to the second's
-    int64_t ld, adv;  // adv: elements from one tile to the next
-    int32_t idx[KM ? 1 : IT];
+    const char *base;               // (scalar) what the offsets of the split's first tile count from
+    int64_t adv;                    // (scalar) bytes from one tile to the next
+    uint32_t off[KM ? 2 * IT : IT];  // the lane's chunks, in bytes
+    int over;                       // not KM: bytes from the first part's columns to the second's
+    int kofs;                       // KM: this thread's chunk in the 128 bytes; else its row of the sum
+    uint32_t pitch, col;            // not KM: bytes of a row, and the lane's columns in it
     RowMap map;
     int64_t pos0;
-    const T *col;     // not KM: the thread's columns in row 0
 
     static __device__ __forceinline__ int mn_turn(int k) { return CPR >= 16 ? (k & 3) << 2 : ((k >> 1) & 1) << 2; }
 
     // KM: rows [r0, r0 + n) of C at positions; out of range rows repeat the last
-    __device__ __forceinline__ void init_km(const T *base, int64_t ld_, const RowMap &m, int64_t r0, int64_t n,
+    __device__ __forceinline__ void init_km(const T *m0, int64_t ld, const RowMap &m, int64_t r0, int64_t n,
                                             int64_t k0) {
         const int row = threadIdx.x >> 3;
         kofs = ((threadIdx.x & 7) ^ ((row >> 1) & 7)) * E;
-        adv = BK;
+        adv = BK * sizeof(T);
+        const bool mapped = m.slots != nullptr;
+        base = (const char *)(m0 + (mapped ? 0 : r0 * ld) + k0);
 #pragma unroll
         for (int i = 0; i < 2 * IT; ++i) {
-            const int64_t r = row + i * STEP;
-            p[i] = base + m(r0 + (r < n ? r : n - 1)) * ld_ + kofs + k0;
+            const int64_t r = row + i * STEP < n ? row + i * STEP : n - 1;
+            off[i] = (uint32_t)(((mapped ? m(r0 + r) : r) * ld + kofs) * (int64_t)sizeof(T));
         }
     }
     // not KM: columns [c0, cols), the sum over positions from pos; out of range
     // columns repeat the last chunk
-    __device__ __forceinline__ void init_mn(const T *base, int64_t ld_, const RowMap &m, int64_t c0, int64_t cols,
+    __device__ __forceinline__ void init_mn(const T *m0, int64_t ld, const RowMap &m, int64_t c0, int64_t cols,
                                             int64_t pos, int64_t k0) {
         kofs = threadIdx.x / CPR;
         const int64_t c = c0 + (int64_t)((threadIdx.x % CPR) ^ mn_turn(kofs)) * E;
         const int64_t lastc = (cols - 1) / E * E;
         const int64_t first = c < lastc ? c : lastc, second = c + PR < lastc ? c + PR : lastc;
-        col = base + first;
-        over = (int)(second - first);
-        ld = ld_;
-        adv = BK * ld;
+        over = (int)(second - first) * (int)sizeof(T);
+        col = (uint32_t)(first * sizeof(T));
+        pitch = (uint32_t)(ld * sizeof(T));
         map = m;
         pos0 = pos;
+        const bool mapped = m.slots != nullptr;
+        adv = mapped ? 0 : BK * ld * (int64_t)sizeof(T);
+        base = (const char *)(m0 + (mapped ? 0 : (pos + k0) * ld));
 #pragma unroll
-        for (int i = 0; i < IT; ++i) p[i] = col + (pos + k0 + kofs + i * STEP) * ld;
+        for (int i = 0; i < IT; ++i) off[i] = (uint32_t)(kofs + i * STEP) * pitch + col;
     }
-    // not KM: the slots of the tile at k0 (kend > 0: where the sum ends).  They
-    // are read as scalars, a wave's few rows at a time: a vector load would
-    // have to be waited for behind all loads to LDS under way.
+    // not KM: turns the slots of the tile at k0 (kend > 0: where the sum ends)
+    // into offsets.  They are read as scalars, a wave's few rows at a time: a
+    // vector load would have to be waited for behind all loads to LDS under way.
     __device__ __forceinline__ void fetch_rows(int64_t k0, int64_t kend, int wave) {
         if constexpr (!KM) {
             if (map.slots != nullptr) {
                 typedef const __attribute__((address_space(4))) int32_t *const_ptr;
                 const const_ptr s = (const_ptr)(uintptr_t)(map.slots + pos0);
                 const int mine = (threadIdx.x & 63) / CPR;
+                int32_t v[IT][RPW];
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
+                for (int i = 0; i < IT; ++i)
 #pragma unroll
                     for (int j = 0; j < RPW; ++j) {
                         const int64_t k = k0 + wave * RPW + i * STEP + j;
-                        const int32_t v = s[k < kend ? k : kend - 1];
-                        idx[i] = j == 0 || mine == j ? v : idx[i];
+                        v[i][j] = s[k < kend ? k : kend - 1];
                     }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    int32_t r = v[i][0];
+#pragma unroll
+                    for (int j = 1; j < RPW; ++j) r = mine == j ? v[i][j] : r;
+                    off[i] = (uint32_t)map.of(r) * pitch + col;
                 }
             }
         }
     }
-    // Load i of a part of the next tile, of which `rem` steps of the sum are
-    // left: zeros past them.  The second part's loads follow the first's.
-    __device__ __forceinline__ void issue(Lds part, int wave, int half, int i, int rem) {
-        const int n = KM ? half * IT + i : i;
-        const T *src = !KM && map.slots != nullptr ? col + map.of(idx[i]) * ld : p[n];
-        if (!KM && half == 1) src += over;
+    // Load i of a part of tile `tile`, every step of which is in the sum
+    __device__ __forceinline__ void issue(const char *from, Lds part, int wave, int half, int i) const {
+        const uint32_t o = KM ? off[half * IT + i] : off[i] + (half ? over : 0);
+        load_to_lds(from, o, part + (i * NT + wave * 64) * E);
+    }
+    // the same where only `rem` steps of it are left: zeros past them
+    __device__ __forceinline__ void issue_end(const char *from, Lds part, int wave, int half, int i, int rem) const {
+        const uint32_t o = KM ? off[half * IT + i] : off[i] + (half ? over : 0);
         const int k = KM ? kofs : kofs + i * STEP;
-        load_to_lds(k < rem ? (const void *)src : (const void *)g_zeros, part + (i * NT + wave * 64) * E);
-        if (KM || half == 1) p[n] += adv;
+        load_to_lds(k < rem ? (const void *)(from + o) : (const void *)g_zeros, part + (i * NT + wave * 64) * E);
     }
     // The lane's 16 bytes for rows (columns) [r0, r0 + 32) of a part and
     // 32-byte step s
@@ -416,32 +450,34 @@ struct Epilogue {
     }
 };
 
-// BS x BS of C a workgroup of WM x WN waves, the sum in tiles of 128 bytes of
+// BS x BS of C a workgroup of 2 x 2 waves, the sum in tiles of 128 bytes of
 // each row, two tiles of both operands in LDS.
 //
-// Each operand's tile lies in two parts, and a wave's block of C takes rows
-// from both parts of A and columns from both parts of B.  A wave goes through
-// a tile in two turns: it reads A's first part and both of B's and multiplies
-// them, then reads A's second part and multiplies that.  A part's place in LDS
-// is refilled, with the tile after the next, as soon as every wave has it in
-// registers, so loads have more than a tile's time to arrive.  Reading and
-// multiplying alternate, with a barrier after each; of two waves on a SIMD one
-// reads while the other multiplies.
-template <typename T, int KIND, int BS, int WM, int WN>
-__global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtiles, int64_t ntiles) {
-    constexpr int NT = WM * WN * 64;
+// Bound by the matrix units: a wave's products take 2048 cycles a tile (BS =
+// 256), and everything else is sent between them.  Each operand's tile lies in
+// two parts, and a wave's block of C takes rows from both parts of A and
+// columns from both parts of B, so a tile is four quarters: A0 B0, A0 B1,
+// A1 B1, A1 B0.  While one quarter is multiplied from registers, the part
+// that the next one lacks is read, and after every two quarters, once all
+// waves have two parts in registers (a barrier), these parts' places are
+// refilled with the tile after the next, four parts ahead of use: loads are
+// spread evenly over the products and have most of two tiles' time to arrive.
+// One wave a SIMD holds 128 x 128 of C in 256 accumulation registers: 8 waves
+// of 128 x 64 read 1.5 times as much from LDS.
+template <typename T, int KIND, int BS>
+__global__ __launch_bounds__(kTileThreads)
+__attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void k_product(LinArgs a, int64_t mtiles,
+                                                                                          int64_t ntiles) {
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int BK = 8 * E;
     constexpr int BM = BS, BN = BS;
-    constexpr int TA = BM / 2 / WM / 32;  // 32-row blocks of a part that a wave takes
-    static_assert(BN / 2 / WN == 32 && TA >= 1, "a wave takes 32 columns of either part of B");
+    constexpr int TB = BS / 128;  // 32-row (column) blocks of a part that a wave takes
     constexpr bool AKM = KIND != kDw, BKM = KIND == kFwd;
-    typedef Operand<T, AKM, BM, NT> OpA;
-    typedef Operand<T, BKM, BN, NT> OpB;
-    constexpr int PART = OpA::PART;
-    static_assert(OpA::PART == OpB::PART && OpA::IT == 2 && OpB::IT == 2, "parts of one size, two loads a thread each");
-    constexpr bool PING = NT == 512;  // two waves a SIMD: half a turn apart
-    // tile t: parts A0, A1, B0, B1 at (t & 1) * 4
+    typedef Operand<T, AKM, BS> OpA;
+    typedef Operand<T, BKM, BS> OpB;
+    constexpr int PART = OpA::PART, IT = OpA::IT;
+    static_assert(OpA::PART == OpB::PART && OpA::IT == OpB::IT, "parts of one size");
+    // A0, A1 of even tiles, A0, A1 of odd ones, then B's
     __shared__ __attribute__((aligned(256))) T smem[8 * PART];
     typedef const __attribute__((address_space(3))) T *Lds;
     const Lds parts = (Lds)smem;
@@ -480,11 +516,14 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         // only the workgroups that have a tile come past this (no barrier yet)
         const bool rest = a.splits == 1;
         TileAt none;
-        const int64_t tiles = find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, -1, none);
+        const int64_t tiles = scalar(find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, -1, none));
         const int64_t id = xcd_tile(blockIdx.x, tiles * ntiles);
         if (id < 0) return;
         nt = id % ntiles;
         find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, id / ntiles, t);
+        t.g = __builtin_amdgcn_readfirstlane(t.g);
+        t.p0 = scalar(t.p0);
+        t.p1 = scalar(t.p1);
         r0 = t.p0;
         nrows = t.p1 - t.p0;
     }
@@ -521,113 +560,131 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         ob.init_mn(Bg, a.ldb, a.bmap, c0, a.N, pos, kbeg);
     }
 
-    // acc[i][j]: row block i of A's first part (i < TA) or second, column
-    // block j of B's parts
-    v16f acc[2 * TA][2];
+    // acc[i][j]: row block i of A's first part (i < TB) or second, column block
+    // j likewise
+    v16f acc[2 * TB][2 * TB];
 #pragma unroll
-    for (int i = 0; i < 2 * TA; ++i)
+    for (int i = 0; i < 2 * TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * TB; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const int wm = wave / WN * (TA * 32), wn = wave % WN * 32;
-    typename Mma<T>::Frag fa[4][TA], fb[4][2];
-    auto read_a = [&](Lds part) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int i = 0; i < TA; ++i) fa[s][i] = OpA::frag(part, wm + i * 32, s);
-    };
-    auto read_b = [&](Lds part) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) fb[s][j] = OpB::frag(part + j * PART, wn, s);
-    };
-    // The end of a reading turn: this wave's reads are in registers (the
-    // compiler's own wait, before the barrier), and of its loads to LDS all but
-    // the latest `later` have arrived (vmcnt, which counts them in order; the
-    // other counters are left alone).
+    const int wm = (wave >> 1) * (TB * 32), wn = (wave & 1) * (TB * 32);
+    // A's first and second part; of B's, tiles take turns in which holds the first
+    typename Mma<T>::Frag fa[2][4][TB], fb[2][4][TB];
+    auto read_a = [&](int to, Lds part, int n) { fa[to][n / TB][n % TB] = OpA::frag(part, wm + n % TB * 32, n / TB); };
+    auto read_b = [&](int to, Lds part, int n) { fb[to][n / TB][n % TB] = OpB::frag(part, wn + n % TB * 32, n / TB); };
+    // All but the latest `later` loads to LDS have arrived, in every wave
+    // (vmcnt, which counts a wave's loads in order; the other counters are left
+    // alone), and every wave has read what it read (the compiler's wait before
+    // the barrier).
     auto landed = [&](auto later) {
         constexpr int n = decltype(later)::value;
         __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
         __syncthreads();
     };
+    // A quarter: A's part I with what fb[B] holds, as B's part J; between the
+    // products the reads of a part and `loads` loads, in this order.
+    auto quarter = [&](auto I, auto B, auto J, auto read, auto load) {
+        constexpr int i0 = decltype(I)::value, b = decltype(B)::value, j0 = decltype(J)::value;
+        constexpr int PRODUCTS = 4 * TB * TB, READS = 4 * TB;
+#pragma unroll
+        for (int n = 0; n < PRODUCTS; ++n) {
+            const int s = n / (TB * TB), i = n / TB % TB, j = n % TB;
+            acc[i0 * TB + i][j0 * TB + j] = Mma<T>::m32(fb[b][s][j], fa[i0][s][i], acc[i0 * TB + i][j0 * TB + j]);
+#pragma unroll
+            for (int r = n * READS / PRODUCTS; r < (n + 1) * READS / PRODUCTS; ++r) read(r);
+#pragma unroll
+            for (int l = n * IT / PRODUCTS; l < (n + 1) * IT / PRODUCTS; ++l) load(l);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    std::integral_constant<int, 0> c0_;
+    std::integral_constant<int, 1> c1_;
+    auto place_a = [&](int odd, int part) { return parts + (odd * 2 + part) * PART; };
+    auto place_b = [&](int odd, int part) { return parts + (4 + odd * 2 + part) * PART; };
     auto rows_of = [&](int64_t i) {
         if constexpr (KIND == kDw) {
             oa.fetch_rows(kbeg + i * BK, ka, wave);
             ob.fetch_rows(kbeg + i * BK, kb, wave);
         }
     };
-    // A multiplying turn on A's first or second part, with `loads` loads of a
-    // later tile spread between the products: the matrix unit stays busy while
-    // they are sent.
-    auto multiply = [&](auto second, auto loads, auto load) {
-        constexpr int I0 = decltype(second)::value * TA, LOADS = decltype(loads)::value;
-        constexpr int PRODUCTS = 4 * TA * 2;
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int n = 0; n < PRODUCTS; ++n) {
-            const int s = n / (2 * TA), i = n / 2 % TA, j = n % 2;
-            acc[I0 + i][j] = Mma<T>::m32(fb[s][j], fa[s][i], acc[I0 + i][j]);
-#pragma unroll
-            for (int l = n * LOADS / PRODUCTS; l < (n + 1) * LOADS / PRODUCTS; ++l) load(l);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_s_setprio(0);
-        if (PING) __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    std::integral_constant<int, 0> none;
-    std::integral_constant<int, 1> one;
-    std::integral_constant<int, 2> two;
-    std::integral_constant<int, 6> six;
-    if (steps > 0) {
-        // A's first part and B's parts of a tile (6 loads), and A's second (2)
-        auto most = [&](Lds tile, int l, int ra, int rb) {
-            if (l < 2) oa.issue(tile, wave, 0, l, ra);
-            else ob.issue(tile + (l < 4 ? 2 : 3) * PART, wave, l < 4 ? 0 : 1, l & 1, rb);
+    // Tile i (odd: ODD): on entry fa[0] and fb[ODD] hold A0 and B0, on exit
+    // those of the next tile (the latter in fb[!ODD]).  END: the tiles it
+    // sends for may lie past the end of the sum.
+    auto tile = [&](auto ODD, auto END, int64_t i) {
+        constexpr int odd = decltype(ODD)::value;
+        constexpr bool end = decltype(END)::value;
+        std::integral_constant<int, 1 - odd> other;
+        rows_of(i + 2);
+        const char *from_a = (const char *)scalar((int64_t)(oa.base + (i + 2) * oa.adv));
+        const char *from_b = (const char *)scalar((int64_t)(ob.base + (i + 2) * ob.adv));
+        const int ra = end ? left(ea, i + 2) : 0, rb = end ? left(eb, i + 2) : 0;
+        auto load_a = [&](int half, int l) {
+            if (end) oa.issue_end(from_a, place_a(odd, half), wave, half, l, ra);
+            else oa.issue(from_a, place_a(odd, half), wave, half, l);
         };
-        rows_of(0);
+        auto load_b = [&](int half, int l) {
+            if (end) ob.issue_end(from_b, place_b(odd, half), wave, half, l, rb);
+            else ob.issue(from_b, place_b(odd, half), wave, half, l);
+        };
+        quarter(c0_, ODD, c0_, [&](int n) { read_b(1 - odd, place_b(odd, 1), n); }, [&](int l) { load_a(0, l); });
+        quarter(c0_, other, c1_, [&](int n) { read_a(1, place_a(odd, 1), n); }, [&](int l) { load_b(0, l); });
+        landed(std::integral_constant<int, 4 * IT>{});
+        quarter(c1_, other, c1_, [&](int n) { read_a(0, place_a(1 - odd, 0), n); }, [&](int l) { load_b(1, l); });
+        quarter(c1_, ODD, c0_, [&](int n) { read_b(1 - odd, place_b(1 - odd, 0), n); }, [&](int l) { load_a(1, l); });
+        landed(std::integral_constant<int, 4 * IT>{});
+    };
+    if (steps > 0) {
+        // both tiles' parts in the order of their use
+        for (int i = 0; i < 2; ++i) {
+            rows_of(i);
+            const char *from_a = oa.base + i * oa.adv, *from_b = ob.base + i * ob.adv;
+            const int ra = left(ea, i), rb = left(eb, i);
 #pragma unroll
-        for (int l = 0; l < 6; ++l) most(parts, l, left(ea, 0), left(eb, 0));
+            for (int l = 0; l < IT; ++l) oa.issue_end(from_a, place_a(i, 0), wave, 0, l, ra);
 #pragma unroll
-        for (int l = 0; l < 2; ++l) oa.issue(parts + PART, wave, 1, l, left(ea, 0));
-        rows_of(1);
+            for (int l = 0; l < IT; ++l) ob.issue_end(from_b, place_b(i, 0), wave, 0, l, rb);
 #pragma unroll
-        for (int l = 0; l < 6; ++l) most(parts + 4 * PART, l, left(ea, 1), left(eb, 1));
-        landed(std::integral_constant<int, 8>{});
-        const bool second = PING && wave >= NT / 128;
-        if (second) __builtin_amdgcn_s_barrier();
-        for (int64_t i = 0; i < steps; ++i) {
-            const Lds tile = parts + (i & 1) * 4 * PART, next = parts + (~i & 1) * 4 * PART;
-            read_a(tile);
-            read_b(tile + 2 * PART);
-            landed(six);  // A's second part of this tile is there
-            const int r1 = left(ea, i + 1);
-            multiply(none, two, [&](int l) { oa.issue(next + PART, wave, 1, l, r1); });
-            rows_of(i + 2);
-            read_a(tile + PART);
-            landed(two);  // the next tile's first part of A and both of B are there
-            const int ra = left(ea, i + 2), rb = left(eb, i + 2);
-            multiply(one, six, [&](int l) { most(tile, l, ra, rb); });
+            for (int l = 0; l < IT; ++l) ob.issue_end(from_b, place_b(i, 1), wave, 1, l, rb);
+#pragma unroll
+            for (int l = 0; l < IT; ++l) oa.issue_end(from_a, place_a(i, 1), wave, 1, l, ra);
         }
-        if (PING && !second) __builtin_amdgcn_s_barrier();
+        landed(std::integral_constant<int, 6 * IT>{});
+#pragma unroll
+        for (int n = 0; n < 4 * TB; ++n) {
+            read_a(0, place_a(0, 0), n);
+            read_b(0, place_b(0, 0), n);
+        }
+        landed(std::integral_constant<int, 4 * IT>{});
+        // two tiles a round; of an odd number the last one's partner is zeros
+        const int64_t whole = (ea < eb ? ea : eb) - kbeg;  // steps of the sum in both
+        int64_t i = 0;
+        for (; (i + 4) * BK <= whole; i += 2) {
+            tile(c0_, std::false_type{}, i);
+            tile(c1_, std::false_type{}, i + 1);
+        }
+        for (; i < steps; i += 2) {
+            tile(c0_, std::true_type{}, i);
+            tile(c1_, std::true_type{}, i + 1);
+        }
     }
-    landed(none);
+    landed(c0_);
 
-    // ---- out: 32 rows of 64 columns a wave at a time through LDS, so that the
-    // rows leave in whole chunks.  A lane holds one row of C and 4 columns
-    // apiece of it (the operands are multiplied the other way round).
-    constexpr int LDS_ROW = 68;
-    static_assert(WM * WN * 32 * LDS_ROW * 4 <= sizeof(smem), "the staged rows fit the tiles");
+    // ---- out: 32 rows of a wave at a time through LDS, so that the rows leave
+    // in whole chunks.  A lane holds one row of C and 4 columns apiece of it
+    // (the operands are multiplied the other way round).
+    constexpr int WIDE = TB * 64;        // columns of a wave
+    constexpr int LDS_ROW = WIDE + 4;
+    constexpr int LPR = WIDE / 8;        // lanes that write a row
+    static_assert(4 * 32 * LDS_ROW * 4 <= sizeof(smem), "the staged rows fit the tiles");
     float *stage = reinterpret_cast<float *>(smem) + wave * 32 * LDS_ROW;
     const int lane = threadIdx.x & 63;
     Epilogue<T> ep;
-    // lanes 0..3 of eight: the wave's columns in B's first part, 4..7: second
-    const int64_t col = c0 + ((lane >> 2) & 1) * (BN / 2) + wn + (lane & 3) * 8;
+    // the first half of a row's lanes: the wave's columns in B's first part
+    const int lc = lane % LPR;
+    const int64_t col = c0 + lc / (LPR / 2) * (BN / 2) + wn + lc % (LPR / 2) * 8;
     if (a.splits > 1 || rest) {
         ep.col = col;
         const int64_t left = a.N - col;
@@ -636,9 +693,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         ep.init(a, t.g, col);
     }
 #pragma unroll
-    for (int i = 0; i < 2 * TA; ++i) {
+    for (int i = 0; i < 2 * TB; ++i) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * TB; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 v4f v;
@@ -650,12 +707,12 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-            const int row = q * 8 + (lane >> 3);
-            const int64_t r = i / TA * (BM / 2) + wm + i % TA * 32 + row;
+        for (int q = 0; q < LPR / 2; ++q) {
+            const int row = q * (64 / LPR) + lane / LPR;
+            const int64_t r = i / TB * (BM / 2) + wm + i % TB * 32 + row;
             float v[8];
-            const v4f lo = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + (lane & 7) * 8);
-            const v4f hi = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + (lane & 7) * 8 + 4);
+            const v4f lo = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + lc * 8);
+            const v4f hi = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + lc * 8 + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[e] = lo[e];
@@ -672,8 +729,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_product(LinArgs a, int64_t mtil
                     else Epilogue<T>::put((T *)a.C + crow * a.ldc + col, v, ep.n);
                     if (a.Z != nullptr) Epilogue<T>::put((T *)a.Z + crow * a.ldz + col, v, ep.n);
                 } else {
-                    ep.out(a, KIND == kDw || a.offsets == nullptr ? (KIND == kDw ? t.g : 0) : t.g,
-                           KIND == kDw ? r0 + r : a.cmap(r0 + r), v);
+                    ep.out(a, t.g, KIND == kDw ? r0 + r : a.cmap(r0 + r), v);
                 }
             }
         }
@@ -965,8 +1021,8 @@ hipError_t run_product(const LinArgs &a, int tile, hipStream_t s) {
     if (grid > 0) {
         if (grid > INT32_MAX) return hipErrorInvalidValue;
         const dim3 gr((unsigned)grid, (unsigned)a.splits);
-        if (tile == 256) k_product<T, KIND, 256, 2, 4><<<gr, 512, 0, s>>>(a, mt, nt);
-        else k_product<T, KIND, 128, 2, 2><<<gr, 256, 0, s>>>(a, mt, nt);
+        if (tile == 256) k_product<T, KIND, 256><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
+        else k_product<T, KIND, 128><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
     }
     if (a.splits > 1) {
         const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
