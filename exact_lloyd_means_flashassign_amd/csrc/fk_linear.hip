@@ -73,32 +73,80 @@ struct Mma<float> {
 
 // ---- activations ----------------------------------------------------------------
 
-// The error function's and tanh's library forms; 1/(1 + e^-z) in a form that
-// does not overflow into NaN (e^-z = inf gives 0).
-__device__ __forceinline__ float activate(int act, float z) {
-    switch (act) {
-    case FK_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case FK_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.707106781f));
-    case FK_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.797884561f * (z + 0.044715f * z * z * z)));
-    case FK_ACT_SILU: return z / (1.0f + expf(-z));
-    default: return z;
+// 2^x and 1/x by the hardware's instructions (about an ulp each); an infinite
+// 2^x gives a logistic of 0.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
+
+// (1 + erf(z / sqrt 2)) / 2 by the rational approximation 7.1.26 of Abramowitz
+// and Stegun, Handbook of Mathematical Functions (1964), whose error is below
+// 1.5e-7 in erf, and e^(-z^2/2), which it needs anyway.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float x = fabsf(z) * 0.707106781f;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    float p = 1.061405429f;
+    p = __builtin_fmaf(p, t, -1.453152027f);
+    p = __builtin_fmaf(p, t, 1.421413741f);
+    p = __builtin_fmaf(p, t, -0.284496736f);
+    p = __builtin_fmaf(p, t, 0.254829592f);
+    e = exp_of(-0.5f * z * z);
+    const float tail = 0.5f * p * t * e;  // the smaller of the two sides
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// twice the argument of gelu_tanh's tanh: z (1 + tanh u) / 2 = z logistic(2 u)
+__device__ __forceinline__ float tanh_arg(float z) { return 1.59576912f * (z + 0.044715f * z * z * z); }
+
+// the activation of N values (the choice outside their loop)
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&z)[N]) {
+    if (act == FK_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = z[i] > 0.0f ? z[i] : (z[i] != z[i] ? z[i] : 0.0f);
+    } else if (act == FK_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float e;
+            z[i] *= normal_cdf(z[i], e);
+        }
+    } else if (act == FK_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] *= logistic(tanh_arg(z[i]));
+    } else if (act == FK_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] *= logistic(z[i]);
     }
 }
 
-__device__ __forceinline__ float act_slope(int act, float z) {
-    switch (act) {
-    case FK_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case FK_ACT_GELU:
-        return 0.5f * (1.0f + erff(z * 0.707106781f)) + z * expf(-0.5f * z * z) * 0.398942280f;
-    case FK_ACT_GELU_TANH: {
-        const float t = tanhf(0.797884561f * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.797884561f * (1.0f + 0.134145f * z * z);
-    }
-    case FK_ACT_SILU: {
-        const float s = 1.0f / (1.0f + expf(-z));
-        return s * (1.0f + z * (1.0f - s));
-    }
-    default: return 1.0f;
+// d[i] *= the activation's slope at z[i].  Where the slope has come to its
+// limit (0 or 1), z is held back so that its powers stay finite.
+template <int N>
+__device__ __forceinline__ void times_slope(int act, const float (&z)[N], float (&d)[N]) {
+    if (act == FK_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = z[i] > 0.0f ? d[i] : (z[i] != z[i] ? z[i] : 0.0f * d[i]);
+    } else if (act == FK_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float c = z[i] != z[i] ? z[i] : fminf(fmaxf(z[i], -64.0f), 64.0f);
+            float e;
+            const float s = normal_cdf(c, e);
+            d[i] *= s + c * e * 0.398942280f;
+        }
+    } else if (act == FK_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float c = z[i] != z[i] ? z[i] : fminf(fmaxf(z[i], -64.0f), 64.0f);
+            const float s = logistic(tanh_arg(c));
+            d[i] *= s + c * s * (1.0f - s) * 1.59576912f * (1.0f + 0.134145f * c * c);
+        }
+    } else if (act == FK_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float c = z[i] != z[i] ? z[i] : fminf(fmaxf(z[i], -128.0f), 128.0f);
+            const float s = logistic(c);
+            d[i] *= s * (1.0f + c * (1.0f - s));
+        }
     }
 }
 
@@ -212,6 +260,7 @@ struct LinArgs {
     int64_t rows, N;           // rows (of a group for kDw) and columns of C
     int64_t ka, kb;            // where the sum ends in A and in B
     int G, act, splits, skip, cf32, bf32;
+    int chunked;               // C, R and Z can be written and read by whole chunks of 8 columns
 };
 
 typedef const __attribute__((address_space(3))) void *lds_at;
@@ -399,9 +448,11 @@ struct Epilogue {
             }
         }
     }
+    // SURE: all eight exist, on whole chunks
+    template <bool SURE = false>
     static __device__ __forceinline__ void put(T *q, const float (&v)[8], int n) {
         constexpr int E = 16 / (int)sizeof(T);
-        if (n == 8 && ((uintptr_t)q & 15) == 0) {
+        if (SURE || (n == 8 && ((uintptr_t)q & 15) == 0)) {
 #pragma unroll
             for (int j = 0; j < 8; j += E) {
                 Chunk<T, E> o;
@@ -414,9 +465,10 @@ struct Epilogue {
                 if (i < n) q[i] = (T)v[i];
         }
     }
+    template <bool SURE = false>
     static __device__ __forceinline__ void get(const T *q, float (&v)[8], int n) {
         constexpr int E = 16 / (int)sizeof(T);
-        if (n == 8 && ((uintptr_t)q & 15) == 0) {
+        if (SURE || (n == 8 && ((uintptr_t)q & 15) == 0)) {
 #pragma unroll
             for (int j = 0; j < 8; j += E) {
                 Chunk<T, E> o;
@@ -428,25 +480,53 @@ struct Epilogue {
             for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)q[i] : 0.0f;
         }
     }
-    // crow: the row of C (kDw: within its group)
-    __device__ __forceinline__ void out(const LinArgs &a, int g, int64_t crow, float (&v)[8]) const {
-        if (n == 0) return;
-        const int64_t at = (int64_t)g * a.gsc + crow * a.ldc + col;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += bias[i];
+    // zeros in row crow of C, and of the pre-activations
+    __device__ __forceinline__ void zero(const LinArgs &a, int64_t crow) const {
+        const float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.cf32) Epilogue<float>::put((float *)a.C + crow * a.ldc + col, v, n);
+        else put((T *)a.C + crow * a.ldc + col, v, n);
         if (a.Z != nullptr) put((T *)a.Z + crow * a.ldz + col, v, n);
-        if (a.act != FK_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = activate(a.act, v[i]);
-        }
+    }
+    // N rows of C, eight columns of each; crow: the row (kDw: within its
+    // group), below 0: none.  SURE: every row and column exists, on whole chunks.
+    template <bool SURE, int N>
+    __device__ __forceinline__ void out(const LinArgs &a, int g, const int64_t (&crow)[N], float (&v)[N * 8]) const {
+        if (!SURE && n == 0) return;
+        float r[N][8];
         if (a.R != nullptr) {
-            float r[8];
-            get((const T *)a.R + crow * a.ldr + col, r, n);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
+            for (int k = 0; k < N; ++k)
+                if (SURE || crow[k] >= 0) get<SURE>((const T *)a.R + crow[k] * a.ldr + col, r[k], n);
         }
-        if (a.cf32) Epilogue<float>::put((float *)a.C + at, v, n);
-        else put((T *)a.C + at, v, n);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k * 8 + i] += bias[i];
+        if (a.Z != nullptr) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (SURE || crow[k] >= 0)
+                    put<SURE>((T *)a.Z + crow[k] * a.ldz + col, *(const float(*)[8])(v + k * 8), n);
+        }
+        activate(a.act, v);
+        if (a.R != nullptr) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k * 8 + i] += r[k][i];
+        }
+        const int64_t first = (int64_t)g * a.gsc + col;
+        if (sizeof(T) != 4 && a.cf32) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (SURE || crow[k] >= 0)
+                    Epilogue<float>::template put<SURE>((float *)a.C + first + crow[k] * a.ldc, *(const float(*)[8])(v + k * 8), n);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (SURE || crow[k] >= 0)
+                    put<SURE>((T *)a.C + first + crow[k] * a.ldc, *(const float(*)[8])(v + k * 8), n);
+        }
     }
 };
 
@@ -593,8 +673,10 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         for (int n = 0; n < PRODUCTS; ++n) {
             const int s = n / (TB * TB), i = n / TB % TB, j = n % TB;
             acc[i0 * TB + i][j0 * TB + j] = Mma<T>::m32(fb[b][s][j], fa[i0][s][i], acc[i0 * TB + i][j0 * TB + j]);
+            // the reads in the first half, so that a barrier at the quarter's end
+            // finds them done
 #pragma unroll
-            for (int r = n * READS / PRODUCTS; r < (n + 1) * READS / PRODUCTS; ++r) read(r);
+            for (int r = 2 * n * READS / PRODUCTS; r < 2 * (n + 1) * READS / PRODUCTS && r < READS; ++r) read(r);
 #pragma unroll
             for (int l = n * IT / PRODUCTS; l < (n + 1) * IT / PRODUCTS; ++l) load(l);
             __builtin_amdgcn_sched_barrier(0);
@@ -672,14 +754,18 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     }
     landed(c0_);
 
-    // ---- out: 32 rows of a wave at a time through LDS, so that the rows leave
-    // in whole chunks.  A lane holds one row of C and 4 columns apiece of it
-    // (the operands are multiplied the other way round).
-    constexpr int WIDE = TB * 64;        // columns of a wave
-    constexpr int LDS_ROW = WIDE + 4;
-    constexpr int LPR = WIDE / 8;        // lanes that write a row
-    static_assert(4 * 32 * LDS_ROW * 4 <= sizeof(smem), "the staged rows fit the tiles");
-    float *stage = reinterpret_cast<float *>(smem) + wave * 32 * LDS_ROW;
+    // ---- out: one part's rows of a wave at a time through LDS, so that the
+    // rows leave in whole chunks.  A lane holds one row of C and 4 columns
+    // apiece of it (the operands are multiplied the other way round).  Chunk c
+    // of row r lies at place c ^ r: both the lanes that write one chunk of many
+    // rows and those that read a row meet different banks.
+    constexpr int CH = TB * 16;          // 16-byte chunks of a staged row
+    constexpr int LPR = CH / 2;          // lanes that write a row of C
+    constexpr int RPP = 64 / LPR;        // rows that a wave writes at once
+    constexpr int ROWS = TB * 32;        // rows of a part
+    constexpr int BATCH = 4;
+    static_assert(4 * ROWS * CH * 16 <= sizeof(smem), "the staged rows fit the tiles");
+    v4f *stage = reinterpret_cast<v4f *>(smem) + wave * ROWS * CH;
     const int lane = threadIdx.x & 63;
     Epilogue<T> ep;
     // the first half of a row's lanes: the wave's columns in B's first part
@@ -692,47 +778,73 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     } else {
         ep.init(a, t.g, col);
     }
+    auto put_part = [&](auto P) {
+        constexpr int p = decltype(P)::value;
 #pragma unroll
-    for (int i = 0; i < 2 * TB; ++i) {
+        for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2 * TB; ++j)
+            for (int j = 0; j < 2 * TB; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v4f v;
+                for (int q = 0; q < 4; ++q) {
+                    v4f v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][q * 4 + e];
-                *reinterpret_cast<v4f *>(stage + (lane & 31) * LDS_ROW + j * 32 + q * 8 + (lane >> 5) * 4) = v;
-            }
+                    for (int e = 0; e < 4; ++e) v[e] = acc[p * TB + i][j][q * 4 + e];
+                    const int row = i * 32 + (lane & 31), c = j * 8 + q * 2 + (lane >> 5);
+                    stage[row * CH + (c ^ (row & (CH - 1)))] = v;
+                }
+    };
+    // every row and column of the tile exists, on whole chunks
+    const bool sure = nrows == BM && c0 + BN <= a.N && a.chunked;
+#pragma unroll 1
+    for (int p = 0; p < 2; ++p) {
+        if (p == 0) put_part(c0_);
+        else put_part(c1_);
         // the wave's own region: its lanes' writes before its lanes' reads
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
+        const int64_t p0 = p * (BM / 2) + wm + lane / LPR;
 #pragma unroll 1
-        for (int q = 0; q < LPR / 2; ++q) {
-            const int row = q * (64 / LPR) + lane / LPR;
-            const int64_t r = i / TB * (BM / 2) + wm + i % TB * 32 + row;
-            float v[8];
-            const v4f lo = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + lc * 8);
-            const v4f hi = *reinterpret_cast<const v4f *>(stage + row * LDS_ROW + lc * 8 + 4);
+        for (int q = 0; q < ROWS; q += BATCH * RPP) {
+            float v[BATCH * 8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = lo[e];
-                v[4 + e] = hi[e];
-            }
-            if (r < nrows) {
-                if (a.splits > 1) {
-                    const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
-                    const int64_t prow = KIND == kDw ? (int64_t)t.g * a.rows + r0 + r : r0 + r;
-                    Epilogue<float>::put(a.part + ((int64_t)split * all + prow) * a.N + ep.col, v, ep.n);
-                } else if (rest) {
-                    const int64_t crow = a.cmap(r0 + r);
-                    if (a.cf32) Epilogue<float>::put((float *)a.C + crow * a.ldc + col, v, ep.n);
-                    else Epilogue<T>::put((T *)a.C + crow * a.ldc + col, v, ep.n);
-                    if (a.Z != nullptr) Epilogue<T>::put((T *)a.Z + crow * a.ldz + col, v, ep.n);
-                } else {
-                    ep.out(a, t.g, KIND == kDw ? r0 + r : a.cmap(r0 + r), v);
+            for (int k = 0; k < BATCH; ++k) {
+                const int row = q + k * RPP + lane / LPR;
+                const v4f lo = stage[row * CH + ((lc * 2) ^ (row & (CH - 1)))];
+                const v4f hi = stage[row * CH + ((lc * 2 + 1) ^ (row & (CH - 1)))];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[k * 8 + e] = lo[e];
+                    v[k * 8 + 4 + e] = hi[e];
                 }
             }
+            int64_t crow[BATCH];
+            if (a.splits > 1) {
+                const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
+                const int64_t first = split * all + (KIND == kDw ? (int64_t)t.g * a.rows : 0) + r0;
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int64_t r = p0 + q + k * RPP;
+                    if (r < nrows)
+                        Epilogue<float>::put(a.part + (first + r) * a.N + col, *(const float(*)[8])(v + k * 8), ep.n);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int64_t r = p0 + q + k * RPP;
+                crow[k] = sure || r < nrows ? (KIND == kDw ? r0 + r : a.cmap(r0 + r)) : -1;
+            }
+            if (rest) {
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+                    if (crow[k] >= 0) ep.zero(a, crow[k]);
+            } else if (sure) {
+                ep.template out<true>(a, t.g, crow, v);
+            } else {
+                ep.template out<false>(a, t.g, crow, v);
+            }
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
 }
@@ -774,9 +886,8 @@ __global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
     Epilogue<T> ep;
     if (rest) {
         ep.n = a.N - col >= 8 ? 8 : (int)(a.N - col);
-        if (a.cf32) Epilogue<float>::put((float *)a.C + crow * a.ldc + col, v, ep.n);
-        else Epilogue<T>::put((T *)a.C + crow * a.ldc + col, v, ep.n);
-        if (a.Z != nullptr) Epilogue<T>::put((T *)a.Z + crow * a.ldz + col, v, ep.n);
+        ep.col = col;
+        ep.zero(a, crow);
         return;
     }
     ep.init(a, g, col);
@@ -786,7 +897,8 @@ __global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += w[i];
     }
-    ep.out(a, g, crow, v);
+    const int64_t rows[1] = {crow};
+    ep.template out<false>(a, g, rows, v);
 }
 
 // ---- a few rows against a whole weight matrix -----------------------------------------
@@ -870,7 +982,8 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
         }
         Epilogue<T> ep;
         ep.init(a, g, n0 + c);
-        ep.out(a, g, a.cmap(p0 + m), v);
+        const int64_t rows[1] = {a.cmap(p0 + m)};
+        ep.template out<false>(a, g, rows, v);
     }
 }
 
@@ -908,8 +1021,7 @@ __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int
             if (a.act != FK_ACT_NONE) {
                 float z[8];
                 Epilogue<T>::get((const T *)a.Z + row * a.ldz + col, z, n);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] *= act_slope(a.act, z[i]);
+                times_slope(a.act, z, d);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -1002,8 +1114,15 @@ __global__ __launch_bounds__(256) void k_pad_rows(const T *in, int64_t ldi, int6
 constexpr int kFewRows = 16;      // most rows of a group that k_product_few takes
 constexpr int kCus = 256;
 
+// Whether eight columns from a multiple of eight on are whole 16-byte chunks.
+bool on_chunks(const void *p, int64_t ld, size_t size) {
+    return p == nullptr || (((uintptr_t)p & 15) == 0 && ld * (int64_t)size % 16 == 0);
+}
+
 template <typename T, int KIND>
-hipError_t run_product(const LinArgs &a, int tile, hipStream_t s) {
+hipError_t run_product(LinArgs a, int tile, hipStream_t s) {
+    a.chunked = on_chunks(a.C, a.ldc, a.cf32 ? 4 : sizeof(T)) && on_chunks(a.C, a.gsc, a.cf32 ? 4 : sizeof(T)) &&
+                on_chunks(a.R, a.ldr, sizeof(T)) && on_chunks(a.Z, a.ldz, sizeof(T));
     const int64_t nt = cdiv(a.N, tile);
     int64_t mt, grid;
     if (KIND == kDw) {
