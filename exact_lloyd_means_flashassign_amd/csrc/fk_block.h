@@ -50,7 +50,7 @@ struct LinearShape {
 struct LinearPlan {
     int64_t M;
     int G;
-    bool few, tiled, pad_x, pad_w, make_dz;
+    bool few, tiled, pad_x, pad_w, sort_x, make_dz;
     int tile, splits, tile_w, splits_w;
     int64_t grad_tiles;
     size_t xpad, wpad, part, dz, colsum, total;

@@ -1092,19 +1092,20 @@ __global__ __launch_bounds__(256) void k_bias_grad(LinArgs a, const float *colsu
     }
 }
 
-// out[r] = in[r] with its columns padded by zeros to ldo (whole chunks): the
+// out[r] = in[map(r)] with its columns padded by zeros to ldo (whole chunks): the
 // tiled product reads 16 bytes at a time, so operands whose rows do not start
 // on 16 bytes are laid out once more first.
 template <typename T>
-__global__ __launch_bounds__(256) void k_pad_rows(const T *in, int64_t ldi, int64_t rows, int64_t cols, T *out,
-                                                  int64_t ldo) {
+__global__ __launch_bounds__(256) void k_pad_rows(const T *in, int64_t ldi, RowMap map, int64_t rows, int64_t cols,
+                                                  T *out, int64_t ldo) {
     constexpr int E = 16 / (int)sizeof(T);
     const int64_t chunks = ldo / E;
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < rows * chunks; id += (int64_t)gridDim.x * 256) {
         const int64_t r = id / chunks, c = id % chunks * E;
+        const T *p = in + map(r) * ldi + c;
         Chunk<T, E> o;
 #pragma unroll
-        for (int i = 0; i < E; ++i) o.e[i] = c + i < cols ? in[r * ldi + c + i] : (T)0.0f;
+        for (int i = 0; i < E; ++i) o.e[i] = c + i < cols ? p[i] : (T)0.0f;
         o.store(out + r * ldo + c);
     }
 }
@@ -1184,6 +1185,18 @@ bool whole(int64_t cols, int64_t ld, int dtype) {
     return cols % e == 0 && ld % e == 0;
 }
 
+// The tiled product reads an operand as it lies if its rows are whole chunks
+// and the 32-bit offsets of its loads reach: over a tile's rows from the
+// tile's first, or, where slots say which rows, over the whole matrix (with
+// 2 GB to spare for what is added within a row).
+constexpr int64_t kReach = (int64_t)1 << 31;
+bool readable(int64_t cols, int64_t ld, int dtype) {
+    return whole(cols, ld, dtype) && ld * 256 * (int64_t)dtype_size(dtype) <= kReach;
+}
+bool reachable(int64_t rows, int64_t ld, int dtype) {
+    return (double)rows * (double)ld * (double)dtype_size(dtype) <= (double)kReach;
+}
+
 }  // namespace
 
 // What a call needs and in which order its scratch is laid out.
@@ -1201,10 +1214,14 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
     };
     p.few = !backward && mean <= kFewRows;
     p.tiled = backward || h.grouped || !p.few;
-    p.pad_x = p.tiled && !whole(h.K, h.ldx, h.dtype);
-    p.pad_w = p.tiled && !whole(h.K, h.ldw, h.dtype);
+    const int64_t kp = cdiv(h.K, bk / 8) * (bk / 8);
+    p.pad_x = p.tiled && !readable(h.K, h.ldx, h.dtype);
+    p.pad_w = p.tiled && !readable(h.K, h.ldw, h.dtype);
+    // X by slots past the loads' reach: laid out in position order
+    p.sort_x = p.tiled && h.grouped && !reachable(h.M / h.share, p.pad_x ? kp : h.ldx, h.dtype);
+    p.pad_x = p.pad_x || p.sort_x;
     const int64_t wrows = groups * h.N;
-    if (p.pad_x) p.xpad = take(pad16(h.M / h.share, h.K, h.dtype));
+    if (p.pad_x) p.xpad = take(pad16(p.sort_x ? h.M : h.M / h.share, h.K, h.dtype));
     if (p.pad_w) p.wpad = take(pad16(wrows, h.K, h.dtype));
     if (!backward) {
         const Shape s = pick_shape(h.grouped ? mean : h.M, h.N, groups, cdiv(h.K, bk));
@@ -1214,7 +1231,8 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
         return p;
     }
     // dZ is laid out in position order unless dY serves as it is
-    p.make_dz = h.act != FK_ACT_NONE || h.ydtype != h.dtype || !whole(h.N, h.ldy, h.dtype);
+    p.make_dz = h.act != FK_ACT_NONE || h.ydtype != h.dtype || !readable(h.N, h.ldy, h.dtype) ||
+                (h.grouped && !reachable(h.M, h.ldy, h.dtype));
     if (p.make_dz) p.dz = take(pad16(h.M, h.N, h.dtype));
     p.grad_tiles = h.grouped ? h.M / kGradRows + (h.G < h.M ? h.G : h.M) : cdiv(h.M, kGradRows);
     p.colsum = take((size_t)p.grad_tiles * h.N * 4);
@@ -1231,12 +1249,19 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
 namespace {
 
 template <typename T>
-hipError_t pad_rows(const void *in, int64_t ldi, int64_t rows, int64_t cols, void *out, hipStream_t s) {
+hipError_t pad_rows(const void *in, int64_t ldi, const RowMap &map, int64_t rows, int64_t cols, void *out, hipStream_t s) {
     constexpr int E = 16 / (int)sizeof(T);
     const int64_t ldo = cdiv(cols, E) * E;
     const int64_t n = cdiv(rows * (ldo / E), 256);
-    if (n > 0) k_pad_rows<T><<<(unsigned)(n < 65536 ? n : 65536), 256, 0, s>>>((const T *)in, ldi, rows, cols, (T *)out, ldo);
+    if (n > 0) k_pad_rows<T><<<(unsigned)(n < 65536 ? n : 65536), 256, 0, s>>>((const T *)in, ldi, map, rows, cols, (T *)out, ldo);
     return hipGetLastError();
+}
+
+// X with padded rows, or in position order (sort_x)
+template <typename T>
+hipError_t lay_out_x(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, char *ws, hipStream_t s) {
+    const RowMap map = p.sort_x ? row_map(b.slots, h.M, h.share) : row_map(nullptr, h.M, 1);
+    return pad_rows<T>(b.X, h.ldx, map, p.sort_x ? h.M : h.M / h.share, h.K, ws + p.xpad, s);
 }
 
 template <typename T>
@@ -1251,6 +1276,7 @@ hipError_t linear_fwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     a.offsets = b.offsets;
     a.amap = row_map(b.slots, h.M, h.share);
     a.cmap = row_map(b.slots, h.M, 1);
+    const RowMap plain = row_map(nullptr, h.M, 1);
     a.M = a.rows = h.M, a.N = h.N, a.G = h.grouped ? h.G : 1, a.act = h.act, a.splits = p.splits;
     a.part = (float *)(ws + p.part);
     hipError_t e = hipSuccess;
@@ -1264,11 +1290,12 @@ hipError_t linear_fwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     a.A = b.X, a.lda = h.ldx, a.B = b.W, a.ldb = h.ldw, a.gsb = h.N * h.ldw;
     a.ka = a.kb = kp;
     if (p.pad_x) {
-        if ((e = pad_rows<T>(b.X, h.ldx, h.M / h.share, h.K, ws + p.xpad, s)) != hipSuccess) return e;
+        if ((e = lay_out_x<T>(h, p, b, ws, s)) != hipSuccess) return e;
         a.A = ws + p.xpad, a.lda = kp;
+        if (p.sort_x) a.amap = plain;
     }
     if (p.pad_w) {
-        e = pad_rows<T>(b.W, h.ldw, a.G * h.N, h.K, ws + p.wpad, s);
+        e = pad_rows<T>(b.W, h.ldw, plain, a.G * h.N, h.K, ws + p.wpad, s);
         if (e != hipSuccess) return e;
         a.B = ws + p.wpad, a.ldb = kp, a.gsb = h.N * kp;
     }
@@ -1298,11 +1325,11 @@ hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     const void *X = b.X, *W = b.W;
     int64_t ldx = h.ldx, ldw = h.ldw;
     if (p.pad_x && b.dW) {
-        if ((e = pad_rows<T>(X, ldx, h.M / h.share, h.K, ws + p.xpad, s)) != hipSuccess) return e;
+        if ((e = lay_out_x<T>(h, p, b, ws, s)) != hipSuccess) return e;
         X = ws + p.xpad, ldx = kp;
     }
     if (p.pad_w && b.dX) {
-        if ((e = pad_rows<T>(W, ldw, G * h.N, h.K, ws + p.wpad, s)) != hipSuccess) return e;
+        if ((e = pad_rows<T>(W, ldw, row_map(nullptr, h.M, 1), G * h.N, h.K, ws + p.wpad, s)) != hipSuccess) return e;
         W = ws + p.wpad, ldw = kp;
     }
     LinArgs a{};
@@ -1317,7 +1344,8 @@ hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
         if ((e = run_product<T, kDx>(a, p.tile, s)) != hipSuccess) return e;
     }
     if (b.dW) {
-        a.B = X, a.ldb = ldx, a.gsb = 0, a.bmap = row_map(b.slots, h.M, h.share);
+        a.B = X, a.ldb = ldx, a.gsb = 0;
+        a.bmap = p.sort_x ? row_map(nullptr, h.M, 1) : row_map(b.slots, h.M, h.share);
         a.C = b.dW, a.ldc = h.K, a.gsc = h.N * h.K, a.cf32 = sizeof(T) == 4;
         a.rows = h.N, a.N = h.K, a.splits = p.splits_w;
         if ((e = run_product<T, kDw>(a, p.tile_w, s)) != hipSuccess) return e;

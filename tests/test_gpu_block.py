@@ -374,6 +374,46 @@ def test_grouped_matches_plain_for_one_group(gpu_lib):
     assert torch.equal(a, b)
 
 
+def test_grouped_rows_past_32_bit_offsets(gpu_lib):
+    """X and dY of more than 4 GB, rows taken from all over them by slots: a
+    sample of rows against float64, dW of one group as a whole."""
+    fk = gpu_lib
+    T, K, N, E = 1_050_007, 2064, 128, 3
+    g = torch.Generator(device=DEV).manual_seed(1)
+    X = torch.empty((T, K), dtype=torch.bfloat16, device=DEV)
+    for i in range(0, T, 100_000):
+        X[i:i + 100_000].normal_(generator=g)
+    assert X.numel() * 2 > 1 << 32
+    Wt = rand(E, N, K, seed=2, scale=K ** -0.5, dtype=torch.bfloat16)
+    ids = torch.randint(0, E + 1, (T,), generator=g, device=DEV, dtype=torch.int32)
+    ids[-5:] = torch.tensor([0, 1, 2, 0, 1], dtype=torch.int32)
+    slots, offsets = fk.fk_sort_inverse(ids, E + 1)
+    where = {"slots": slots, "offsets": offsets}
+    Y, _ = fk.fk_linear(X, Wt, **where)
+    at = torch.cat((torch.arange(0, T, 30011, device=DEV), torch.arange(T - 5, T, device=DEV)))
+    for e in range(E + 1):
+        rows = at[ids[at] == e]
+        x = X[rows].double()
+        w = Wt[e].double() if e < E else torch.zeros((N, K), dtype=R.D, device=DEV)
+        bound = (K + 24) * R.W * (x.abs() @ w.abs().t())
+        check(f"Y of group {e}", Y[rows], (x @ w.t()).cpu(), bound.cpu(), torch.bfloat16)
+    dY = rand(T, N, seed=5, dtype=torch.bfloat16)
+    dX, dW, dB = fk.fk_linear_backward(dY, X, Wt, **where)
+    for e in range(E):
+        rows = at[ids[at] == e]
+        d, w = dY[rows].double(), Wt[e].double()
+        check(f"dX of group {e}", dX[rows], (d @ w).cpu(), ((N + 24) * R.W * (d.abs() @ w.abs())).cpu(), torch.bfloat16)
+    rows = (ids == 1).nonzero()[:, 0]
+    want = torch.zeros((N, K), dtype=R.D, device=DEV)
+    mag = torch.zeros((N, K), dtype=R.D, device=DEV)
+    for part in rows.split(50_000):
+        d, x = dY[part].double(), X[part].double()
+        want += d.t() @ x
+        mag += d.abs().t() @ x.abs()
+    check("dW", dW[1], want.cpu(), ((rows.numel() + 24) * R.W * mag).cpu(), torch.bfloat16)
+    assert not dX[ids == E].any()
+
+
 # ---- combine -----------------------------------------------------------------------------
 
 
