@@ -102,7 +102,7 @@ template <int N>
 __device__ __forceinline__ void activate(int act, float (&z)[N]) {
     if (act == FK_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = z[i] > 0.0f ? z[i] : (z[i] != z[i] ? z[i] : 0.0f);
+        for (int i = 0; i < N; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
     } else if (act == FK_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -124,7 +124,7 @@ template <int N>
 __device__ __forceinline__ void times_slope(int act, const float (&z)[N], float (&d)[N]) {
     if (act == FK_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = z[i] > 0.0f ? d[i] : (z[i] != z[i] ? z[i] : 0.0f * d[i]);
+        for (int i = 0; i < N; ++i) d[i] *= z[i] > 0.0f ? 1.0f : 0.0f;
     } else if (act == FK_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -489,14 +489,25 @@ struct Epilogue {
     }
     // N rows of C, eight columns of each; crow: the row (kDw: within its
     // group), below 0: none.  SURE: every row and column exists, on whole chunks.
+    // SURE comes with the residual's chunks, which were sent for earlier.
+    struct Eight {
+        Chunk<T, 16 / (int)sizeof(T)> c[sizeof(T) / 2];
+    };
     template <bool SURE, int N>
-    __device__ __forceinline__ void out(const LinArgs &a, int g, const int64_t (&crow)[N], float (&v)[N * 8]) const {
+    __device__ __forceinline__ void out(const LinArgs &a, int g, const int64_t (&crow)[N], float (&v)[N * 8],
+                                        const Eight *res) const {
         if (!SURE && n == 0) return;
         float r[N][8];
         if (a.R != nullptr) {
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (SURE || crow[k] >= 0) get<SURE>((const T *)a.R + crow[k] * a.ldr + col, r[k], n);
+            for (int k = 0; k < N; ++k) {
+                if (SURE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[k][i] = (float)res[k].c[i * (int)sizeof(T) / 16].e[i % (16 / (int)sizeof(T))];
+                } else if (crow[k] >= 0) {
+                    get((const T *)a.R + crow[k] * a.ldr + col, r[k], n);
+                }
+            }
         }
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -752,8 +763,6 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
             tile(c1_, std::true_type{}, i + 1);
         }
     }
-    landed(c0_);
-
     // ---- out: one part's rows of a wave at a time through LDS, so that the
     // rows leave in whole chunks.  A lane holds one row of C and 4 columns
     // apiece of it (the operands are multiplied the other way round).  Chunk c
@@ -763,7 +772,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     constexpr int LPR = CH / 2;          // lanes that write a row of C
     constexpr int RPP = 64 / LPR;        // rows that a wave writes at once
     constexpr int ROWS = TB * 32;        // rows of a part
-    constexpr int BATCH = 4;
+    constexpr int BATCH = 4;  // rows a lane takes at a time
     static_assert(4 * ROWS * CH * 16 <= sizeof(smem), "the staged rows fit the tiles");
     v4f *stage = reinterpret_cast<v4f *>(smem) + wave * ROWS * CH;
     const int lane = threadIdx.x & 63;
@@ -794,11 +803,42 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                 }
     };
     // every row and column of the tile exists, on whole chunks
-    const bool sure = nrows == BM && c0 + BN <= a.N && a.chunked;
+    const bool sure = nrows == BM && c0 + BN <= a.N && a.chunked && !rest && a.splits == 1;
+    auto row_at = [&](int p, int q, int k) {
+        const int64_t r = r0 + p * (BM / 2) + wm + lane / LPR + q + k * RPP;
+        return KIND == kDw ? r : a.cmap(r);
+    };
+    // the residual of a batch, sent for a batch ahead
+    typename Epilogue<T>::Eight res[BATCH];
+    const bool added = sure && a.R != nullptr;
+    auto send_for = [&](int p, int q) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const T *from = (const T *)a.R + row_at(p, q, k) * a.ldr + col;
+#pragma unroll
+            for (int c = 0; c < (int)sizeof(T) / 2; ++c) res[k].c[c].load(from + c * E);
+        }
+    };
+    // the tiles are read to the end, and no load to LDS is under way
+    if (added) {
+        send_for(0, 0);
+        landed(std::integral_constant<int, BATCH * (int)sizeof(T) / 2>{});
+    } else {
+        landed(c0_);
+    }
 #pragma unroll 1
     for (int p = 0; p < 2; ++p) {
-        if (p == 0) put_part(c0_);
-        else put_part(c1_);
+        // (the empty statements keep the compiler from making one block of the
+        // two, which would select between all the accumulators)
+        if (p == 0) {
+            asm volatile("; first part");
+            put_part(c0_);
+            asm volatile("; first part staged");
+        } else {
+            asm volatile("; second part");
+            put_part(c1_);
+            asm volatile("; second part staged");
+        }
         // the wave's own region: its lanes' writes before its lanes' reads
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -817,7 +857,6 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                     v[k * 8 + 4 + e] = hi[e];
                 }
             }
-            int64_t crow[BATCH];
             if (a.splits > 1) {
                 const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
                 const int64_t first = split * all + (KIND == kDw ? (int64_t)t.g * a.rows : 0) + r0;
@@ -829,19 +868,29 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                 }
                 continue;
             }
+            int64_t crow[BATCH];
+            if (sure) {
+                typename Epilogue<T>::Eight now[BATCH];
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int64_t r = p0 + q + k * RPP;
-                crow[k] = sure || r < nrows ? (KIND == kDw ? r0 + r : a.cmap(r0 + r)) : -1;
+                for (int k = 0; k < BATCH; ++k) {
+                    crow[k] = row_at(p, q, k);
+                    now[k] = res[k];
+                }
+                if (added) {
+                    if (q + BATCH * RPP < ROWS) send_for(p, q + BATCH * RPP);
+                    else if (p == 0) send_for(1, 0);
+                }
+                ep.template out<true>(a, t.g, crow, v, now);
+                continue;
             }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) crow[k] = p0 + q + k * RPP < nrows ? row_at(p, q, k) : -1;
             if (rest) {
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k)
                     if (crow[k] >= 0) ep.zero(a, crow[k]);
-            } else if (sure) {
-                ep.template out<true>(a, t.g, crow, v);
             } else {
-                ep.template out<false>(a, t.g, crow, v);
+                ep.template out<false>(a, t.g, crow, v, nullptr);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -898,7 +947,7 @@ __global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
         for (int i = 0; i < 8; ++i) v[i] += w[i];
     }
     const int64_t rows[1] = {crow};
-    ep.template out<false>(a, g, rows, v);
+    ep.template out<false>(a, g, rows, v, nullptr);
 }
 
 // ---- a few rows against a whole weight matrix -----------------------------------------
@@ -983,7 +1032,7 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
         Epilogue<T> ep;
         ep.init(a, g, n0 + c);
         const int64_t rows[1] = {a.cmap(p0 + m)};
-        ep.template out<false>(a, g, rows, v);
+        ep.template out<false>(a, g, rows, v, nullptr);
     }
 }
 
