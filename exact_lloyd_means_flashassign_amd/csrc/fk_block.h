@@ -22,8 +22,8 @@ hipError_t launch_sum_partials(const float *part, int P, int64_t ld, int64_t spl
                                hipStream_t s);
 
 // ---- router (fk_route.hip) ---------------------------------------------------
-// Workgroups of the forward pass, each leaving one partial row: E column sums
-// of the probabilities and E counts, then live rows and the sum of lse^2.
+// Workgroups of the forward pass, each leaving one partial row: column sums of
+// the probabilities and of lse^2, counts and live rows.
 int route_blocks(int64_t T, int E);
 size_t route_scratch_bytes(int64_t T, int E);
 hipError_t launch_route(int dtype, const void *logits, int64_t ldl, int64_t T, int E, int k, int norm,

@@ -9,13 +9,19 @@
 //   dl = p (v - p.v) + dz 2 lse p / n + the gates' part,   v_e = dbalance E f_e / n
 //   gates over the chosen: g (dg - g.dg);  gates = p: p_i (dg_i - sum_j p_j dg_j)
 //
-// Bound by memory at many rows (each logit read once a pass, its gradient
-// written once) and by the launch at few.  A row belongs to a team of 2^m
-// lanes, 8 consecutive experts a lane up to E = 512 (16 beyond), so a row's
-// reductions are at most six lane exchanges and a lane meets the same experts
-// in every row: the columns' sums and counts stay in its registers until the
-// workgroup is done, and leave as one partial row, which a second kernel adds
-// in a fixed order (a single workgroup finishes by itself).  No atomics.
+// A row belongs to a team of 2^m lanes, 8 consecutive experts a lane up to
+// E = 512 (16 beyond), so a row's reductions are at most six lane exchanges and
+// a lane meets the same experts in every row: the columns' sums stay in its
+// registers until the workgroup is done (the counts in LDS, by integer adds,
+// whose order does not matter), and leave as one partial row, which a second
+// kernel adds in a fixed order (a single workgroup finishes by itself).
+//
+// The k best: a lane turns its logits into keys (below) and sorts them by a
+// network; then the team takes the largest of its lanes' first keys k times,
+// the lane that had it moving on to its next.  A key is the logit as a double,
+// which leaves 29 bits of its fraction free, with the expert's index in the
+// lowest 10, so that one comparison settles ties too and names the expert.
+// At many rows this arithmetic, not memory, is the forward pass's bound.
 //
 // Selection compares logits as they are (no rounding), the lower index first
 // on ties; a row that is not valid or has nothing above -inf is not live: its
@@ -42,7 +48,7 @@ struct RouteArgs {
     const int32_t *ids_in, *counts_in, *live_in;
     const float *d_gates, *d_losses;
     void *d_logits;
-    float *part;  // [blocks][2 E + 2]: probability sums, lse^2, then (as int32) counts, live rows
+    float *part;  // [blocks][part_row(E)]
     int64_t T, ldl;
     int E, k, norm, vec;
 };
@@ -63,9 +69,80 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 template <int LPR>
 __device__ __forceinline__ float row_max(float v) {
+    return lanes_reduce<LPR>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// ---- keys ----
+constexpr uint32_t kIndexBits = 1023;  // FK_MAX_EXPERTS - 1
+constexpr double kNoKey = -__builtin_inf();
+
+// The larger the logit the larger the key, then the lower the index: the
+// index is turned round where a larger fraction makes a larger number.  -inf
+// and NaN have no key; +inf stands as 2^128.
+__device__ __forceinline__ double key_of(float l, int e) {
+    if (!(l > -INFINITY)) return kNoKey;
+    const double d = l == INFINITY ? 0x1p128 : (double)(l + 0.0f);  // (-0 is 0)
+    uint64_t u = __builtin_bit_cast(uint64_t, d);
+    u |= (u >> 63) ? (uint32_t)e : kIndexBits - (uint32_t)e;
+    return __builtin_bit_cast(double, u);
+}
+__device__ __forceinline__ int key_expert(double k) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, k);
+    const uint32_t i = (uint32_t)u & kIndexBits;
+    return (int)((u >> 63) ? i : kIndexBits - i);
+}
+__device__ __forceinline__ float key_logit(double k) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, k) & ~(uint64_t)kIndexBits;
+    return (float)__builtin_bit_cast(double, u);
+}
+
+template <int O>
+__device__ __forceinline__ double key_neighbour(double k) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, k);
+    const uint64_t r = (uint64_t)neighbour<O>((uint32_t)(u >> 32)) << 32 | neighbour<O>((uint32_t)u);
+    return __builtin_bit_cast(double, r);
+}
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
+template <int LPR, int O = 1>
+__device__ __forceinline__ double key_max(double k) {
+    if constexpr (O >= LPR) return k;
+    else return key_max<LPR, 2 * O>(larger(k, key_neighbour<O>(k)));
+}
+
+// Sorts 8 keys, largest first, by a network of 19 comparisons.
+__device__ __forceinline__ void sort8(double *k) {
+    constexpr int net[19][2] = {{0, 2}, {1, 3}, {4, 6}, {5, 7}, {0, 4}, {1, 5}, {2, 6}, {3, 7}, {0, 1}, {2, 3},
+                                {4, 5}, {6, 7}, {2, 4}, {3, 5}, {1, 4}, {3, 6}, {1, 2}, {3, 4}, {5, 6}};
 #pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    for (int i = 0; i < 19; ++i) {
+        const double a = k[net[i][0]], b = k[net[i][1]];
+        k[net[i][0]] = larger(a, b);
+        k[net[i][1]] = smaller(a, b);
+    }
+}
+// ... and 16, as two sorted eights merged: the larger halves of a and of b
+// turned round form a bitonic run each, which three rounds sort.
+__device__ __forceinline__ void sort16(double *k) {
+    sort8(k);
+    sort8(k + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double a = k[i], b = k[15 - i];
+        k[i] = larger(a, b);
+        k[15 - i] = smaller(a, b);
+    }
+#pragma unroll
+    for (int h = 0; h < 16; h += 8)
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i & o) continue;
+                const double a = k[h + i], b = k[h + i + o];
+                k[h + i] = larger(a, b);
+                k[h + i + o] = smaller(a, b);
+            }
 }
 
 template <typename T, int VPL>
@@ -87,97 +164,83 @@ __device__ __forceinline__ void load_row(const RouteArgs &a, int64_t row, int co
     }
 }
 
-// The largest of the row's values that are not yet taken (bit v of `taken` for
-// the lane's value v) and its expert, the lowest on ties; -1 if nothing above
-// -inf is left.
-template <int VPL, int LPR>
-__device__ __forceinline__ void next_best(const float (&l)[VPL], uint32_t taken, int col, float &best, int &at) {
-    best = -INFINITY;
-    at = -1;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        const bool better = !((taken >> v) & 1u) && l[v] > best;
-        best = better ? l[v] : best;
-        at = better ? col + v : at;
-    }
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) {
-        const float ov = __shfl_xor(best, o, 64);
-        const int oa = __shfl_xor(at, o, 64);
-        const bool take = ov > best || (ov == best && (uint32_t)oa < (uint32_t)at);
-        best = take ? ov : best;
-        at = take ? oa : at;
-    }
-}
+// A partial row: fp32 sums of p for each expert and of lse^2, up to a multiple
+// of four columns; then int32 counts for each expert and live rows, likewise.
+__host__ __device__ inline int part_floats(int E) { return (E + 1 + 3) / 4 * 4; }
+__host__ __device__ inline int part_row(int E) { return 2 * part_floats(E); }
 
-// The counts, live rows and losses from P partial rows, by one workgroup.
+// The counts, live rows and losses from P partial rows, by one workgroup: 4
+// columns a thread, the rows in as many runs as there are threads for, each
+// run's loads in flight together.
 __device__ __forceinline__ void route_finish(const RouteArgs &a, int P, float *sm) {
-    const int E = a.E, ld = 2 * E + 2;
-    int *si = reinterpret_cast<int *>(sm);
-    // columns [0, E]: fp32 (sums of p, sum of lse^2); (E, 2 E + 1]: counts and live rows.
-    // Up to 16 runs of rows a column, added in run order.
-    const int cols = ld;
-    int down = kRouteThreads / 64;
-    __shared__ float s_n[1];
-    float bal = 0.0f;
-    __shared__ float s_tot[16];
-    float *colsum = sm + down * 64;
-    for (int c0 = 0; c0 < cols; c0 += 64) {
-        const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
-        const int c = c0 + lane;
-        float fs = 0.0f;
-        int is = 0;
-        if (c < cols) {
-            for (int p = run; p < P; p += down) {
-                const float v = a.part[(size_t)p * ld + c];
-                if (c <= E) fs += v;
-                else is += __float_as_int(v);
+    const int E = a.E, F = part_floats(E), chunks = 2 * F / 4;
+    const int runs = kRouteThreads / chunks;
+    const int c = threadIdx.x % chunks, run = threadIdx.x / chunks;
+    float4 f = {0.0f, 0.0f, 0.0f, 0.0f};
+    int4 n = {0, 0, 0, 0};
+    const float4 *part = reinterpret_cast<const float4 *>(a.part);
+    if (run < runs) {
+        constexpr int U = 8;
+        for (int p0 = run; p0 < P; p0 += U * runs) {
+            float4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = p0 + u * runs;
+                v[u] = p < P ? part[(size_t)p * chunks + c] : float4{0.0f, 0.0f, 0.0f, 0.0f};
             }
-        }
-        __syncthreads();
-        if (c <= E) sm[run * 64 + lane] = fs;
-        else si[run * 64 + lane] = is;
-        __syncthreads();
-        if (run == 0 && c < cols) {
-            if (c <= E) {
-                float t = 0.0f;
-                for (int r = 0; r < down; ++r) t += sm[r * 64 + lane];
-                colsum[c] = t;
-            } else {
-                int t = 0;
-                for (int r = 0; r < down; ++r) t += si[r * 64 + lane];
-                reinterpret_cast<int *>(colsum)[c] = t;
-                if (c < ld - 1) a.counts[c - E - 1] = t;
-                else a.live[0] = t;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                f.x += v[u].x, f.y += v[u].y, f.z += v[u].z, f.w += v[u].w;
+                n.x += __float_as_int(v[u].x), n.y += __float_as_int(v[u].y);
+                n.z += __float_as_int(v[u].z), n.w += __float_as_int(v[u].w);
             }
         }
     }
+    // the runs in order; sm: [runs][2 F] and then the totals [2 F]
+    float4 *s4 = reinterpret_cast<float4 *>(sm);
     __syncthreads();
-    const int *ci = reinterpret_cast<const int *>(colsum) + E + 1;
-    // total slots and E sum_e counts_e psum_e
-    float tot = 0.0f;
+    const bool whole = c * 4 >= F;  // integer columns
+    if (run < runs)
+        s4[run * chunks + c] = whole ? float4{__int_as_float(n.x), __int_as_float(n.y), __int_as_float(n.z), __int_as_float(n.w)} : f;
+    __syncthreads();
+    float *tot = sm + runs * 2 * F;
+    for (int col = threadIdx.x; col < 2 * F; col += kRouteThreads) {
+        float t = 0.0f;
+        int m = 0;
+        for (int r = 0; r < runs; ++r) {
+            const float v = sm[r * 2 * F + col];
+            t += v;
+            m += __float_as_int(v);
+        }
+        tot[col] = col < F ? t : __int_as_float(m);
+        if (col >= F && col < F + E) a.counts[col - F] = m;
+        if (col == F + E) a.live[0] = m;
+    }
+    __syncthreads();
+    const int *cnt = reinterpret_cast<const int *>(tot) + F;
+    // all slots, and sum_e counts_e psum_e
+    float all = 0.0f, bal = 0.0f;
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-        tot += (float)ci[e];
-        bal += (float)ci[e] * colsum[e];
+        all += (float)cnt[e];
+        bal += (float)cnt[e] * tot[e];
     }
-    tot = lanes_sum<64>(tot);
+    all = lanes_sum<64>(all);
     bal = lanes_sum<64>(bal);
-    __syncthreads();
+    __shared__ float s_all[kRouteThreads / 64], s_bal[kRouteThreads / 64];
     if ((threadIdx.x & 63) == 0) {
-        s_tot[threadIdx.x >> 6] = tot;
-        sm[threadIdx.x >> 6] = bal;
+        s_all[threadIdx.x >> 6] = all;
+        s_bal[threadIdx.x >> 6] = bal;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
         float t = 0.0f, b = 0.0f;
         for (int w = 0; w < kRouteThreads / 64; ++w) {
-            t += s_tot[w];
-            b += sm[w];
+            t += s_all[w];
+            b += s_bal[w];
         }
-        const float n = (float)(ci[E] > 0 ? ci[E] : 1);
-        s_n[0] = n;
-        a.losses[0] = (float)E * (b / (t > 0.0f ? t : 1.0f)) / n;
-        a.losses[1] = colsum[E] / n;
+        const float live = (float)(cnt[E] > 0 ? cnt[E] : 1);
+        a.losses[0] = (float)E * (b / (t > 0.0f ? t : 1.0f)) / live;
+        a.losses[1] = tot[E] / live;
     }
 }
 
@@ -185,22 +248,30 @@ template <typename T, int LPR, int VPL>
 __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     constexpr int RPB = kRouteThreads / LPR;  // rows a round
     constexpr int COLS = LPR * VPL;
-    extern __shared__ float sm[];
+    extern __shared__ __attribute__((aligned(16))) float sm[];
     const int lane = threadIdx.x % LPR;
     const int col = lane * VPL;
+    int *counts = reinterpret_cast<int *>(sm) + COLS;
+    for (int i = threadIdx.x; i < 2 * COLS; i += kRouteThreads) sm[i] = 0.0f;  // (0 as an integer too)
+    __syncthreads();
     float psum[VPL];
-    int cnt[VPL];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        psum[v] = 0.0f;
-        cnt[v] = 0;
-    }
+    for (int v = 0; v < VPL; ++v) psum[v] = 0.0f;
     float zsum = 0.0f;
     int nlive = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < a.T; row += (int64_t)gridDim.x * RPB) {
-        const bool valid = a.valid == nullptr || a.valid[row] != 0;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+    // the next row's logits are under way while this one is worked on
+    float ahead[VPL];
+    auto fetch = [&](int64_t r) {
+        load_row<T, VPL>(a, r, col, r < a.T && (a.valid == nullptr || a.valid[r] != 0), ahead);
+    };
+    fetch(row);
+    for (; row < a.T; row += step) {
         float l[VPL];
-        load_row<T, VPL>(a, row, col, valid, l);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) l[v] = ahead[v];
+        fetch(row + step);
         float m = -INFINITY;
         bool nan = false;
 #pragma unroll
@@ -210,64 +281,64 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         }
         m = row_max<LPR>(m);
         const float nans = row_sum<LPR>(nan ? 1.0f : 0.0f);
-        const bool on = m != -INFINITY || nans > 0.0f;
-        if (on) {
-            float e[VPL], s = 0.0f;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v) {
-                e[v] = exp_neg(l[v] - m);
-                s += e[v];
+        int32_t *ids = a.ids + row * a.k;
+        float *gates = a.gates + row * a.k;
+        if (m == -INFINITY && nans == 0.0f) {
+            for (int j = lane; j < a.k; j += LPR) {
+                ids[j] = a.E;
+                gates[j] = 0.0f;
             }
-            s = row_sum<LPR>(s);
-            const float inv = 1.0f / s;
+            continue;
+        }
+        float e[VPL], s = 0.0f;
+        double key[VPL];
 #pragma unroll
-            for (int v = 0; v < VPL; ++v) psum[v] += e[v] * inv;
-            if (lane == 0) {
-                const float lse = m + logf(s);
-                zsum += lse * lse;
-                ++nlive;
-            }
-            // the k best in turn; the gates' sum over the chosen ones follows
-            uint32_t taken = 0;
-            float gsum = 0.0f;
-            float mine = 0.0f;  // lane j of the team keeps gate j (several passes if k > LPR)
-            for (int j0 = 0; j0 < a.k; j0 += LPR) {
-                const int jn = a.k - j0 < LPR ? a.k - j0 : LPR;
-                int myid = a.E;
-                mine = 0.0f;
-                for (int j = 0; j < jn; ++j) {
-                    float best;
-                    int at;
-                    next_best<VPL, LPR>(l, taken, col, best, at);
-                    const float ge = at >= 0 ? exp_neg(best - m) : 0.0f;
-                    gsum += ge;
+        for (int v = 0; v < VPL; ++v) {
+            e[v] = exp_neg(l[v] - m);
+            s += e[v];
+            key[v] = key_of(l[v], col + v);
+        }
+        s = row_sum<LPR>(s);
+        const float inv = 1.0f / s;
 #pragma unroll
-                    for (int v = 0; v < VPL; ++v) {
-                        const bool here = at == col + v;
-                        taken |= here ? 1u << v : 0u;
-                        cnt[v] += here ? 1 : 0;
-                    }
-                    if (lane == j) {
-                        mine = ge;
-                        myid = at >= 0 ? at : a.E;
-                    }
-                }
-                if (lane < jn) {
-                    a.ids[row * a.k + j0 + lane] = myid;
-                    a.gates[row * a.k + j0 + lane] = mine;  // scaled below
+        for (int v = 0; v < VPL; ++v) psum[v] += e[v] * inv;
+        if (lane == 0) {
+            const float lse = m + logf(s);
+            zsum += lse * lse;
+            ++nlive;
+        }
+        if constexpr (VPL == 8) sort8(key);
+        else sort16(key);
+        // Lane j % LPR of the team keeps choice j and looks at it once LPR of
+        // them are made (gates are written before their scale is known if
+        // there are more, and scaled by the lane that wrote them).
+        float gsum = 0.0f, mine = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += LPR) {
+            const int jn = a.k - j0 < LPR ? a.k - j0 : LPR;
+            double chosen = kNoKey;
+            for (int j = 0; j < jn; ++j) {
+                const double best = key_max<LPR>(key[0]);
+                chosen = lane == j ? best : chosen;
+                if (key[0] == best) {  // keys differ: the lane that had it (or none is left)
+#pragma unroll
+                    for (int v = 0; v + 1 < VPL; ++v) key[v] = key[v + 1];
+                    key[VPL - 1] = kNoKey;
                 }
             }
-            const float scale = a.norm == FK_GATES_CHOSEN ? 1.0f / gsum : inv;
-            // (a lane rewrites only what it wrote itself)
-            for (int j = lane; j < a.k; j += LPR) {
-                const float g = j >= a.k - (a.k - 1) % LPR - 1 ? mine : a.gates[row * a.k + j];
-                a.gates[row * a.k + j] = g == 0.0f ? 0.0f : g * scale;
+            const bool any = chosen != kNoKey;
+            const int at = any ? key_expert(chosen) : a.E;
+            mine = any ? exp_neg(key_logit(chosen) - m) : 0.0f;
+            gsum += row_sum<LPR>(mine);
+            if (any) atomicAdd(&counts[at], 1);
+            if (lane < jn) {
+                ids[j0 + lane] = at;
+                if (a.k > LPR) gates[j0 + lane] = mine;
             }
-        } else {
-            for (int j = lane; j < a.k; j += LPR) {
-                a.ids[row * a.k + j] = a.E;
-                a.gates[row * a.k + j] = 0.0f;
-            }
+        }
+        const float scale = a.norm == FK_GATES_CHOSEN ? 1.0f / gsum : inv;
+        for (int j = lane; j < a.k; j += LPR) {
+            const float g = a.k > LPR ? gates[j] : mine;
+            gates[j] = g == 0.0f ? 0.0f : g * scale;
         }
     }
     // the teams' columns: lanes of a wave that own the same experts, then the
@@ -275,10 +346,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
 #pragma unroll
-        for (int o = LPR; o < 64; o <<= 1) {
-            psum[v] += __shfl_xor(psum[v], o, 64);
-            cnt[v] += __shfl_xor(cnt[v], o, 64);
-        }
+        for (int o = LPR; o < 64; o <<= 1) psum[v] += __shfl_xor(psum[v], o, 64);
     }
     zsum = lanes_sum<64>(zsum);
 #pragma unroll
@@ -287,15 +355,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     const int wv = threadIdx.x >> 6;
     __shared__ float s_z[WV];
     __shared__ int s_live[WV];
-    int *si = reinterpret_cast<int *>(sm) + COLS;
     for (int w = 0; w < WV; ++w) {
         if (w == wv) {
             if ((threadIdx.x & 63) < LPR) {
 #pragma unroll
-                for (int v = 0; v < VPL; ++v) {
-                    sm[col + v] = (w ? sm[col + v] : 0.0f) + psum[v];
-                    si[col + v] = (w ? si[col + v] : 0) + cnt[v];
-                }
+                for (int v = 0; v < VPL; ++v) sm[col + v] += psum[v];
             }
             if ((threadIdx.x & 63) == 0) {
                 s_z[w] = zsum;
@@ -304,20 +368,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         }
         __syncthreads();
     }
-    float *out = a.part + (size_t)blockIdx.x * (2 * a.E + 2);
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
-        out[e] = sm[e];
-        out[a.E + 1 + e] = __int_as_float(si[e]);
-    }
-    if (threadIdx.x == 0) {
+    const int F = part_floats(a.E);
+    float *out = a.part + (size_t)blockIdx.x * 2 * F;
+    for (int c = threadIdx.x; c < F; c += kRouteThreads) {
         float z = 0.0f;
         int n = 0;
-        for (int w = 0; w < WV; ++w) {
-            z += s_z[w];
-            n += s_live[w];
+        if (c == a.E) {
+            for (int w = 0; w < WV; ++w) {
+                z += s_z[w];
+                n += s_live[w];
+            }
         }
-        out[a.E] = z;
-        out[2 * a.E + 1] = __int_as_float(n);
+        out[c] = c < a.E ? sm[c] : z;
+        out[F + c] = __int_as_float(c < a.E ? counts[c] : n);
     }
     if (gridDim.x == 1) {
         __syncthreads();  // the partial row is read back by the same workgroup
@@ -326,15 +389,20 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
 }
 
 __global__ __launch_bounds__(kRouteThreads) void k_route_finish(RouteArgs a, int P) {
-    extern __shared__ float sm[];
+    extern __shared__ __attribute__((aligned(16))) float sm[];
     route_finish(a, P, sm);
 }
 
+// A lane j % LPR of the team takes choice j: it reads that logit again, the
+// team sums what the gates' softmax needs, and the choices' parts reach the
+// lanes that own the experts through LDS.
 template <typename T, int LPR, int VPL>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
     constexpr int RPB = 256 / LPR;
+    __shared__ __attribute__((aligned(16))) float parts[256 * VPL];
     const int lane = threadIdx.x % LPR;
     const int col = lane * VPL;
+    float *own = parts + threadIdx.x * VPL, *team = own - col;
     const float n = (float)(a.live_in[0] > 0 ? a.live_in[0] : 1);
     const float dbal = a.d_losses ? a.d_losses[0] : 0.0f, dz = a.d_losses ? a.d_losses[1] : 0.0f;
     // v_e = dbalance E f_e / n of this lane's experts
@@ -374,49 +442,44 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
             s = row_sum<LPR>(s);
             pv = row_sum<LPR>(pv);
             const float inv = 1.0f / s;
-            const float lse = m + logf(s);
-            const float shift = dz * 2.0f * lse / n - pv * inv;
-            // the gates: dg of the chosen experts, which are marked in `sel`
-            float dg[VPL];
-            uint32_t sel = 0;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v) dg[v] = 0.0f;
+            float shift = -pv * inv;
+            if (dz != 0.0f) shift += dz * 2.0f * (m + logf(s)) / n;
             if (a.d_gates != nullptr) {
-                for (int j = 0; j < a.k; ++j) {
-                    const int at = a.ids_in[row * a.k + j] - col;
-                    if ((unsigned)at < (unsigned)VPL) {
-                        const float g = a.d_gates[row * a.k + j];
-#pragma unroll
-                        for (int v = 0; v < VPL; ++v) {
-                            dg[v] = at == v ? g : dg[v];
-                            sel |= at == v ? 1u << v : 0u;
-                        }
-                    }
+                const int32_t *ids = a.ids_in + row * a.k;
+                const float *dg = a.d_gates + row * a.k;
+                const T *again = (const T *)a.logits + row * a.ldl;
+                float es = 0.0f, in = 0.0f;
+                for (int j = lane; j < a.k; j += LPR) {
+                    const int id = ids[j];
+                    if ((unsigned)id >= (unsigned)a.E) continue;
+                    const float ej = exp_neg((float)again[id] - m);
+                    es += ej;
+                    in += ej * dg[j];
                 }
-            }
-            float es = 0.0f, in = 0.0f;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v) {
-                if ((sel >> v) & 1u) {
-                    es += e[v];
-                    in += e[v] * dg[v];
-                }
-            }
-            in = row_sum<LPR>(in);
-            if (a.norm == FK_GATES_CHOSEN) {
                 es = row_sum<LPR>(es);
-                const float ginv = es > 0.0f ? 1.0f / es : 0.0f;
-                const float inner = in * ginv;
+                in = row_sum<LPR>(in);
+                const bool chosen = a.norm == FK_GATES_CHOSEN;
+                const float scale = chosen ? (es > 0.0f ? 1.0f / es : 0.0f) : inv;
+                const float inner = in * scale;
 #pragma unroll
-                for (int v = 0; v < VPL; ++v) {
-                    const float g = (sel >> v) & 1u ? e[v] * ginv * (dg[v] - inner) : 0.0f;
-                    dl[v] = e[v] * inv * (f[v] + shift) + g;
+                for (int v = 0; v < VPL; ++v) own[v] = 0.0f;
+                // (the team's lanes are in one wave: their LDS accesses are in order)
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                for (int j = lane; j < a.k; j += LPR) {
+                    const int id = ids[j];
+                    if ((unsigned)id >= (unsigned)a.E) continue;
+                    const float g = exp_neg((float)again[id] - m) * scale;
+                    team[id] = chosen ? g * (dg[j] - inner) : g * dg[j];
                 }
-            } else {
-                const float inner = in * inv;
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int v = 0; v < VPL; ++v) dl[v] = e[v] * inv * (f[v] + shift + dg[v] - inner);
+                for (int v = 0; v < VPL; ++v) dl[v] = own[v];
+                if (!chosen) shift -= inner;
             }
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) dl[v] += e[v] * inv * (f[v] + shift);
         }
         T *out = (T *)a.d_logits + row * a.E + col;
         constexpr int W = 16 / (int)sizeof(T);
@@ -446,7 +509,9 @@ template <typename T, bool BWD>
 hipError_t dispatch_route(const RouteArgs &a, hipStream_t s) {
     const int lpr = lanes_per_row(a.E);
     const int vpl = a.E > 512 ? 16 : 8;
-    const size_t need = (size_t)(kRouteThreads + 2 * a.E + 2) * 4, cols = (size_t)lpr * vpl * 8;
+    // the sums and counts of every column; the finish's runs and totals
+    const int row = part_row(a.E), runs = kRouteThreads / (row / 4);
+    const size_t need = (size_t)(runs + 1) * row * 4, cols = (size_t)lpr * vpl * 8;
     const size_t lds = need > cols ? need : cols;
     const int64_t per = 256 / lpr;
     const unsigned bgrid = (unsigned)(cdiv(a.T, per) < 4096 ? cdiv(a.T, per) : 4096);
@@ -493,7 +558,7 @@ int route_blocks(int64_t T, int E) {
     return (int)(need < kRouteMaxBlocks ? need : kRouteMaxBlocks);
 }
 
-size_t route_scratch_bytes(int64_t T, int E) { return (size_t)route_blocks(T, E) * (2 * E + 2) * 4; }
+size_t route_scratch_bytes(int64_t T, int E) { return (size_t)route_blocks(T, E) * part_row(E) * 4; }
 
 hipError_t launch_route(int dtype, const void *logits, int64_t ldl, int64_t T, int E, int k, int norm,
                         const uint8_t *valid, int32_t *ids, float *gates, int32_t *counts, float *losses,

@@ -62,13 +62,54 @@ __device__ __forceinline__ void load_param(const void *p, bool f32, int64_t at, 
     }
 }
 
+// ---- lane exchanges ----
+// Step O of a reduction over aligned groups of lanes, each lane of a group of
+// O holding the same value: v of the neighbouring group of O.  Up to 16 lanes
+// these are data-parallel moves of the vector ALU (quad permutations and
+// mirrors), beyond them the row swaps; none goes through LDS.
+template <int O>
+__device__ __forceinline__ uint32_t neighbour(uint32_t v) {
+    if constexpr (O == 1) {
+        return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);  // quad [1, 0, 3, 2]
+    } else if constexpr (O == 2) {
+        return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);  // quad [2, 3, 0, 1]
+    } else if constexpr (O == 4) {
+        return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);  // mirror of 8
+    } else if constexpr (O == 8) {
+        return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);  // mirror of 16
+    } else {
+        return __shfl_xor(v, O, 64);
+    }
+}
+template <int O>
+__device__ __forceinline__ float neighbour(float v) {
+    return __uint_as_float(neighbour<O>(__float_as_uint(v)));
+}
+
+// combine(own, neighbour's) over groups of W lanes
+template <int W, int O = 1, typename F>
+__device__ __forceinline__ float lanes_reduce(float v, F combine) {
+    if constexpr (O >= W) {
+        return v;
+    } else if constexpr (O >= 16) {
+        // both operands the same: the first result holds the even rows' values
+        // in both rows of a pair, the second the odd rows'
+        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+        const uint32_t u = __float_as_uint(v);
+        v2u r;
+        if constexpr (O == 16) r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(u, u, false, false));
+        else r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+        return lanes_reduce<W, 2 * O>(combine(__uint_as_float(r[0]), __uint_as_float(r[1])), combine);
+    } else {
+        return lanes_reduce<W, 2 * O>(combine(v, neighbour<O>(v)), combine);
+    }
+}
+
 // Sum over aligned groups of W consecutive lanes (W a power of two up to 64);
-// every lane gets it, in the same order in each.
+// every lane gets the same.
 template <int W>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < W; o <<= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    return lanes_reduce<W>(v, [](float a, float b) { return a + b; });
 }
 
 // NV sums over a team of TEAM lanes: one wave, or the 256 threads of the
