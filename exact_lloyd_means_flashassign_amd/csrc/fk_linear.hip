@@ -288,6 +288,11 @@ __device__ __forceinline__ void load_to_lds(const void *src, lds_at lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"((glb_ptr)src), "s"(at)
                  : "m0");
 }
+// 4 bytes a lane
+__device__ __forceinline__ void dword_to_lds(const void *src, lds_at lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"((glb_ptr)src), "s"(at) : "m0");
+}
 #pragma clang diagnostic pop
 
 constexpr int kTileThreads = 256;  // 4 waves, one a SIMD
@@ -314,7 +319,6 @@ struct Operand {
     static constexpr int IT = PR * 8 / NT;              // loads a thread for a part
     static constexpr int CPR = KM ? 8 : PR / E;         // chunks a LDS row
     static constexpr int STEP = NT / CPR;               // LDS rows a load of all threads covers
-    static constexpr int RPW = 64 / CPR;                // LDS rows a load of one wave covers
     const char *base;               // (scalar) what the offsets of the split's first tile count from
     int64_t adv;                    // (scalar) bytes from one tile to the next
     uint32_t off[KM ? 2 * IT : IT];  // the lane's chunks, in bytes
@@ -359,31 +363,38 @@ struct Operand {
 #pragma unroll
         for (int i = 0; i < IT; ++i) off[i] = (uint32_t)(kofs + i * STEP) * pitch + col;
     }
-    // not KM: turns the slots of the tile at k0 (kend > 0: where the sum ends)
-    // into offsets.  They are read as scalars, a wave's few rows at a time: a
-    // vector load would have to be waited for behind all loads to LDS under way.
-    __device__ __forceinline__ void fetch_rows(int64_t k0, int64_t kend, int wave) {
+    // not KM, rows by slots: a wave keeps the slots of four tiles in LDS, 64
+    // places each.  A tile's slots are sent for four tiles ahead (send_rows),
+    // read three ahead (read_rows) and turned into the offsets of the loads
+    // (take_rows) when these are due.  A scalar load instead would make every
+    // LDS read of the wave wait for it, a vector load would wait for all loads
+    // to LDS under way.
+    typedef const __attribute__((address_space(3))) int32_t *Ring;
+    static constexpr int kRing = 4 * 64;
+    Ring ring;
+    int32_t slot[KM ? 1 : IT];
+    // (kend > 0: where the sum ends)
+    __device__ __forceinline__ void send_rows(int64_t tile, int64_t k0, int64_t kend) const {
         if constexpr (!KM) {
             if (map.slots != nullptr) {
-                typedef const __attribute__((address_space(4))) int32_t *const_ptr;
-                const const_ptr s = (const_ptr)(uintptr_t)(map.slots + pos0);
-                const int mine = (threadIdx.x & 63) / CPR;
-                int32_t v[IT][RPW];
+                const int64_t k = k0 + (threadIdx.x & 63);
+                dword_to_lds(map.slots + pos0 + (k < kend ? k : kend - 1), ring + (tile & 3) * 64);
+            }
+        }
+    }
+    __device__ __forceinline__ void read_rows(int64_t tile) {
+        if constexpr (!KM) {
+            if (map.slots != nullptr) {
 #pragma unroll
-                for (int i = 0; i < IT; ++i)
+                for (int i = 0; i < IT; ++i) slot[i] = ring[(tile & 3) * 64 + kofs + i * STEP];
+            }
+        }
+    }
+    __device__ __forceinline__ void take_rows() {
+        if constexpr (!KM) {
+            if (map.slots != nullptr) {
 #pragma unroll
-                    for (int j = 0; j < RPW; ++j) {
-                        const int64_t k = k0 + wave * RPW + i * STEP + j;
-                        v[i][j] = s[k < kend ? k : kend - 1];
-                    }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    int32_t r = v[i][0];
-#pragma unroll
-                    for (int j = 1; j < RPW; ++j) r = mine == j ? v[i][j] : r;
-                    off[i] = (uint32_t)map.of(r) * pitch + col;
-                }
+                for (int i = 0; i < IT; ++i) off[i] = (uint32_t)map.of(slot[i]) * pitch + col;
             }
         }
     }
@@ -570,6 +581,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     static_assert(OpA::PART == OpB::PART && OpA::IT == OpB::IT, "parts of one size");
     // A0, A1 of even tiles, A0, A1 of odd ones, then B's
     __shared__ __attribute__((aligned(256))) T smem[8 * PART];
+    __shared__ __attribute__((aligned(256))) int32_t rings[KIND == kDw ? 4 * 2 * OpA::kRing : 1];
     typedef const __attribute__((address_space(3))) T *Lds;
     const Lds parts = (Lds)smem;
 
@@ -697,10 +709,22 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     std::integral_constant<int, 1> c1_;
     auto place_a = [&](int odd, int part) { return parts + (odd * 2 + part) * PART; };
     auto place_b = [&](int odd, int part) { return parts + (4 + odd * 2 + part) * PART; };
-    auto rows_of = [&](int64_t i) {
+    auto send_rows = [&](int64_t i) {
         if constexpr (KIND == kDw) {
-            oa.fetch_rows(kbeg + i * BK, ka, wave);
-            ob.fetch_rows(kbeg + i * BK, kb, wave);
+            oa.send_rows(i, kbeg + i * BK, ka);
+            ob.send_rows(i, kbeg + i * BK, kb);
+        }
+    };
+    auto read_rows = [&](int64_t i) {
+        if constexpr (KIND == kDw) {
+            oa.read_rows(i);
+            ob.read_rows(i);
+        }
+    };
+    auto take_rows = [&]() {
+        if constexpr (KIND == kDw) {
+            oa.take_rows();
+            ob.take_rows();
         }
     };
     // Tile i (odd: ODD): on entry fa[0] and fb[ODD] hold A0 and B0, on exit
@@ -710,7 +734,8 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         constexpr int odd = decltype(ODD)::value;
         constexpr bool end = decltype(END)::value;
         std::integral_constant<int, 1 - odd> other;
-        rows_of(i + 2);
+        take_rows();
+        send_rows(i + 4);
         const char *from_a = (const char *)scalar((int64_t)(oa.base + (i + 2) * oa.adv));
         const char *from_b = (const char *)scalar((int64_t)(ob.base + (i + 2) * ob.adv));
         const int ra = end ? left(ea, i + 2) : 0, rb = end ? left(eb, i + 2) : 0;
@@ -725,14 +750,24 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         quarter(c0_, ODD, c0_, [&](int n) { read_b(1 - odd, place_b(odd, 1), n); }, [&](int l) { load_a(0, l); });
         quarter(c0_, other, c1_, [&](int n) { read_a(1, place_a(odd, 1), n); }, [&](int l) { load_b(0, l); });
         landed(std::integral_constant<int, 4 * IT>{});
+        read_rows(i + 3);
         quarter(c1_, other, c1_, [&](int n) { read_a(0, place_a(1 - odd, 0), n); }, [&](int l) { load_b(1, l); });
         quarter(c1_, ODD, c0_, [&](int n) { read_b(1 - odd, place_b(1 - odd, 0), n); }, [&](int l) { load_a(1, l); });
         landed(std::integral_constant<int, 4 * IT>{});
     };
     if (steps > 0) {
+        if constexpr (KIND == kDw) {
+            oa.ring = (typename OpA::Ring)rings + wave * 2 * OpA::kRing;
+            ob.ring = (typename OpB::Ring)rings + (wave * 2 + 1) * OpB::kRing;
+            if (oa.map.slots != nullptr || ob.map.slots != nullptr) {
+                for (int i = 0; i < 4; ++i) send_rows(i);
+                landed(c0_);
+            }
+        }
         // both tiles' parts in the order of their use
         for (int i = 0; i < 2; ++i) {
-            rows_of(i);
+            read_rows(i);
+            take_rows();
             const char *from_a = oa.base + i * oa.adv, *from_b = ob.base + i * ob.adv;
             const int ra = left(ea, i), rb = left(eb, i);
 #pragma unroll
@@ -744,6 +779,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
 #pragma unroll
             for (int l = 0; l < IT; ++l) oa.issue_end(from_a, place_a(i, 1), wave, 1, l, ra);
         }
+        read_rows(2);
         landed(std::integral_constant<int, 6 * IT>{});
 #pragma unroll
         for (int n = 0; n < 4 * TB; ++n) {
