@@ -472,6 +472,7 @@ struct Epilogue {
                 o.store(q + j);
             }
         } else {
+#pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i < n) q[i] = (T)v[i];
         }
@@ -488,6 +489,7 @@ struct Epilogue {
                 for (int i = 0; i < E; ++i) v[j + i] = (float)o.e[i];
             }
         } else {
+#pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)q[i] : 0.0f;
         }
     }
@@ -575,6 +577,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     constexpr int BM = BS, BN = BS;
     constexpr int TB = BS / 128;  // 32-row (column) blocks of a part that a wave takes
     constexpr bool AKM = KIND != kDw, BKM = KIND == kFwd;
+    constexpr bool SPLITS = BS == 128;  // sums are split where there are few tiles: never large ones
     typedef Operand<T, AKM, BS> OpA;
     typedef Operand<T, BKM, BS> OpB;
     constexpr int PART = OpA::PART, IT = OpA::IT;
@@ -617,7 +620,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         nrows = a.rows - r0 < BM ? a.rows - r0 : BM;
     } else {
         // only the workgroups that have a tile come past this (no barrier yet)
-        const bool rest = a.splits == 1;
+        const bool rest = !SPLITS || a.splits == 1;
         TileAt none;
         const int64_t tiles = scalar(find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, -1, none));
         const int64_t id = xcd_tile(blockIdx.x, tiles * ntiles);
@@ -636,7 +639,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     // the part of the sum that this split takes, in tiles
     const int64_t kall = ka > kb ? ka : kb;
     int64_t steps = (kall + BK - 1) / BK;
-    if (a.splits > 1) {
+    if (SPLITS && a.splits > 1) {
         const int64_t each = (steps + a.splits - 1) / a.splits;
         kbeg = split * each * BK;
         const int64_t left = steps - split * each;
@@ -799,6 +802,72 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
             tile(c1_, std::true_type{}, i + 1);
         }
     }
+    const int lane = threadIdx.x & 63;
+    constexpr bool PLAIN = KIND != kFwd && sizeof(T) == 2;
+    if constexpr (PLAIN) {
+        // ---- out, without an epilogue: the wave's block, rounded, goes through
+        // LDS at once, so that the rows leave in whole chunks.  A lane holds one
+        // row of C and 4 columns apiece of it (the operands are multiplied the
+        // other way round).  Chunk c of row r lies at place c ^ r, so that
+        // neither the lanes that write one chunk of many rows nor those that
+        // read a row meet on a bank.
+        if (!SPLITS || a.splits == 1) {
+            constexpr int CH = TB * 8;       // 16-byte chunks of a row
+            constexpr int ROWS = TB * 64;
+            constexpr int RPP = 64 / CH;     // rows that a wave writes at once
+            static_assert(4 * ROWS * CH * 16 <= sizeof(smem), "the staged rows fit the tiles");
+            typedef T Four __attribute__((ext_vector_type(4)));
+            T *stage = smem + wave * ROWS * CH * E;
+            landed(c0_);
+#pragma unroll
+            for (int i = 0; i < 2 * TB; ++i)
+#pragma unroll
+                for (int j = 0; j < 2 * TB; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        Four v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = (T)acc[i][j][q * 4 + e];
+                        const int row = i * 32 + (lane & 31);
+                        *(Four *)(stage + (row * CH + ((j * 4 + q) ^ (row & (CH - 1)))) * E + (lane >> 5) * 4) = v;
+                        // (a few accumulators at a time: all at once do not fit)
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            const int lc = lane % CH;
+            const int64_t col = c0 + lc / (CH / 2) * (BN / 2) + wn + lc % (CH / 2) * 8;
+            const int64_t gone = a.N - col;
+            const int n = gone >= 8 ? 8 : (gone > 0 ? (int)gone : 0);
+            T *out = (T *)a.C + (rest ? 0 : (int64_t)t.g * a.gsc) + col;
+            const bool sure = nrows == BM && c0 + BN <= a.N && a.chunked;
+#pragma unroll 1
+            for (int q = 0; q < ROWS; q += 8 * RPP) {
+                Chunk<T, E> v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = q + k * RPP + lane / CH;
+                    v[k].load(stage + (row * CH + (lc ^ (row & (CH - 1)))) * E);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = q + k * RPP + lane / CH;
+                    const int64_t r = row / (TB * 32) * (BM / 2) + wm + row % (TB * 32);
+                    if (!sure && (r >= nrows || n == 0)) continue;
+                    T *to = out + (KIND == kDw ? r0 + r : a.cmap(r0 + r)) * a.ldc;
+                    if (sure || (n == 8 && a.chunked)) {
+                        v[k].store(to);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < n) to[e] = v[k].e[e];
+                    }
+                }
+            }
+            return;
+        }
+    }
+    if constexpr (!PLAIN || SPLITS) {
     // ---- out: one part's rows of a wave at a time through LDS, so that the
     // rows leave in whole chunks.  A lane holds one row of C and 4 columns
     // apiece of it (the operands are multiplied the other way round).  Chunk c
@@ -811,12 +880,11 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     constexpr int BATCH = 4;  // rows a lane takes at a time
     static_assert(4 * ROWS * CH * 16 <= sizeof(smem), "the staged rows fit the tiles");
     v4f *stage = reinterpret_cast<v4f *>(smem) + wave * ROWS * CH;
-    const int lane = threadIdx.x & 63;
     Epilogue<T> ep;
     // the first half of a row's lanes: the wave's columns in B's first part
     const int lc = lane % LPR;
     const int64_t col = c0 + lc / (LPR / 2) * (BN / 2) + wn + lc % (LPR / 2) * 8;
-    if (a.splits > 1 || rest) {
+    if ((SPLITS && a.splits > 1) || rest) {
         ep.col = col;
         const int64_t left = a.N - col;
         ep.n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
@@ -836,10 +904,11 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                     for (int e = 0; e < 4; ++e) v[e] = acc[p * TB + i][j][q * 4 + e];
                     const int row = i * 32 + (lane & 31), c = j * 8 + q * 2 + (lane >> 5);
                     stage[row * CH + (c ^ (row & (CH - 1)))] = v;
+                    __builtin_amdgcn_sched_barrier(0);
                 }
     };
     // every row and column of the tile exists, on whole chunks
-    const bool sure = nrows == BM && c0 + BN <= a.N && a.chunked && !rest && a.splits == 1;
+    const bool sure = nrows == BM && c0 + BN <= a.N && a.chunked && !rest && (!SPLITS || a.splits == 1);
     auto row_at = [&](int p, int q, int k) {
         const int64_t r = r0 + p * (BM / 2) + wm + lane / LPR + q + k * RPP;
         return KIND == kDw ? r : a.cmap(r);
@@ -893,7 +962,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                     v[k * 8 + 4 + e] = hi[e];
                 }
             }
-            if (a.splits > 1) {
+            if (SPLITS && a.splits > 1) {
                 const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
                 const int64_t first = split * all + (KIND == kDw ? (int64_t)t.g * a.rows : 0) + r0;
 #pragma unroll
@@ -931,6 +1000,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
+    }
     }
 }
 
@@ -1256,7 +1326,7 @@ Shape pick_shape(int64_t rows, int64_t cols, int64_t groups, int64_t steps) {
     s.tile = rows > 128 && big >= kCus * 3 / 4 ? 256 : 128;
     const int64_t tiles = cdiv(rows, s.tile) * cdiv(cols, s.tile) * groups;
     s.splits = 1;
-    while (s.splits < 16 && tiles * s.splits * 2 <= kCus && steps / (s.splits * 2) >= 4) s.splits *= 2;
+    while (s.tile == 128 && s.splits < 16 && tiles * s.splits * 2 <= kCus && steps / (s.splits * 2) >= 4) s.splits *= 2;
     return s;
 }
 
