@@ -521,12 +521,46 @@ def _rows(t, name, dtypes, shape=None):
     return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
 
 
-def _one_device(*tensors):
-    """The tensors' device, which the call runs on."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"tensors are on different devices: {sorted(map(str, devices))}")
-    return devices.pop()
+def _one_device(first, *rest) -> int:
+    """Index of the tensors' device, which the call runs on."""
+    d = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"tensors are on different devices: {first.device} and {t.device}")
+    return d
+
+
+def _at(t):
+    """The address of a tensor, or None."""
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle by device index, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _run(fn, d, *args):
+    """fn(*args, current stream of device d) with d current; raises on an error."""
+    stream = _raw_stream(d)
+    if torch.cuda.current_device() == d:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(d):
+            status = fn(*args, stream)
+    if status != 0:
+        _check(status)
+
+
+def _scratch(nbytes, d, workspace):
+    """_workspace for device index d."""
+    if workspace is None:
+        buf = _ws_cache.get((d, _raw_stream(d)))
+        if buf is not None and buf.numel() >= nbytes + 256:
+            base = buf.data_ptr()
+            pad = -base % 256
+            return base + pad, buf.numel() - pad
+    return _workspace(nbytes, torch.device("cuda", d), workspace)
 
 
 _FLOATS = tuple(DTYPES)
@@ -554,14 +588,14 @@ def fk_layer_norm(X, weight=None, bias=None, eps: float = 1e-5, Y=None):
         raise ValueError("weight and bias must be of one type")
     wdt = DTYPES[params[0].dtype if params else X.dtype]
     if Y is None:
-        Y = torch.empty((rows, d), dtype=X.dtype, device=X.device)
-    ldy = _rows(Y, "Y", (X.dtype,), (rows, d))
+        Y, ldy = torch.empty((rows, d), dtype=X.dtype, device=X.device), d
+    else:
+        ldy = _rows(Y, "Y", (X.dtype,), (rows, d))
     mean = torch.empty(rows, dtype=torch.float32, device=X.device)
     rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
     dev = _one_device(X, weight, bias, Y)
-    with torch.cuda.device(dev):
-        _check(load().fk_layer_norm(DTYPES[X.dtype], wdt, _ptr(X), ldx, rows, d, _ptr(weight), _ptr(bias), float(eps),
-                                    _ptr(Y), ldy, _ptr(mean), _ptr(rstd), _stream(dev)))
+    _run(load().fk_layer_norm, dev, DTYPES[X.dtype], wdt, _at(X), ldx, rows, d, _at(weight), _at(bias), float(eps),
+         _at(Y), ldy, _at(mean), _at(rstd))
     return Y, mean, rstd
 
 
@@ -582,13 +616,10 @@ def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = Tru
         dw = torch.empty_like(weight)
         db = torch.empty_like(weight) if with_bias else None
     dev = _one_device(dY, X, mean, rstd, weight, dX)
-    with torch.cuda.device(dev):
-        need = load().fk_layer_norm_backward_workspace_size(rows, d) or 256
-        p, n = _workspace(need, dev, workspace)
-        _check(load().fk_layer_norm_backward(DTYPES[X.dtype], DTYPES[X.dtype if weight is None else weight.dtype],
-                                             _ptr(dY), ldd, _ptr(X), ldx, rows, d, _ptr(mean), _ptr(rstd),
-                                             _ptr(weight), _ptr(dX), lddx, _ptr(dw), _ptr(db), ctypes.c_void_p(p),
-                                             ctypes.c_size_t(n), _stream(dev)))
+    need = load().fk_layer_norm_backward_workspace_size(rows, d) or 256
+    p, n = _scratch(need, dev, workspace)
+    _run(load().fk_layer_norm_backward, dev, DTYPES[X.dtype], DTYPES[X.dtype if weight is None else weight.dtype],
+         _at(dY), ldd, _at(X), ldx, rows, d, _at(mean), _at(rstd), _at(weight), _at(dX), lddx, _at(dw), _at(db), p, n)
     return dX, dw, db
 
 
@@ -612,17 +643,15 @@ def fk_route(logits, k: int, norm="chosen", valid=None, workspace=None):
     k = int(k)
     _valid_mask(valid, T)
     dev = _one_device(logits, valid)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-    gates = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    losses = torch.empty(2, dtype=torch.float32, device=dev)
-    live = torch.empty(1, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        need = load().fk_route_workspace_size(T, E) or 256
-        p, n = _workspace(need, dev, workspace)
-        _check(load().fk_route(DTYPES[logits.dtype], _ptr(logits), ldl, T, E, k, _named(GATES, norm, "gate norm"),
-                               _ptr(valid), _ptr(ids), _ptr(gates), _ptr(counts), _ptr(losses), _ptr(live),
-                               ctypes.c_void_p(p), ctypes.c_size_t(n), _stream(dev)))
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+    gates = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    counts = torch.empty(E, dtype=torch.int32, device=logits.device)
+    losses = torch.empty(2, dtype=torch.float32, device=logits.device)
+    live = torch.empty(1, dtype=torch.int32, device=logits.device)
+    need = load().fk_route_workspace_size(T, E) or 256
+    p, n = _scratch(need, dev, workspace)
+    _run(load().fk_route, dev, DTYPES[logits.dtype], _at(logits), ldl, T, E, k, _named(GATES, norm, "gate norm"),
+         _at(valid), _at(ids), _at(gates), _at(counts), _at(losses), _at(live), p, n)
     return ids, gates, counts, losses, live
 
 
@@ -642,11 +671,9 @@ def fk_route_backward(logits, ids, counts, live, d_gates=None, d_losses=None, no
         _dev(d_losses, "d_losses", torch.float32, (2,))
     _valid_mask(valid, T)
     dev = _one_device(logits, ids, counts, live, d_gates, d_losses, valid)
-    d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(load().fk_route_backward(DTYPES[logits.dtype], _ptr(logits), ldl, T, E, k,
-                                        _named(GATES, norm, "gate norm"), _ptr(valid), _ptr(ids), _ptr(counts),
-                                        _ptr(live), _ptr(d_gates), _ptr(d_losses), _ptr(d_logits), _stream(dev)))
+    d_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _run(load().fk_route_backward, dev, DTYPES[logits.dtype], _at(logits), ldl, T, E, k, _named(GATES, norm,
+         "gate norm"), _at(valid), _at(ids), _at(counts), _at(live), _at(d_gates), _at(d_losses), _at(d_logits))
     return d_logits
 
 
@@ -696,8 +723,11 @@ def fk_linear(X, W, bias=None, act="none", residual=None, slots=None, offsets=No
     h = _linear_problem(X, W, act, slots, offsets, share)
     shape = (h.M, h.N)
     if Y is None:
+        if out_dtype not in (None, X.dtype, torch.float32):
+            raise ValueError(f"out_dtype must be {X.dtype} or torch.float32")
         Y = torch.empty(shape, dtype=out_dtype or X.dtype, device=X.device)
-    h.ldy = _rows(Y, "Y", (X.dtype, torch.float32), shape)
+    else:
+        h.ldy = _rows(Y, "Y", (X.dtype, torch.float32), shape)
     h.ydtype = DTYPES[Y.dtype]
     if out_dtype is not None and Y.dtype != out_dtype:
         raise ValueError(f"Y is {Y.dtype}, out_dtype {out_dtype}")
@@ -708,12 +738,10 @@ def fk_linear(X, W, bias=None, act="none", residual=None, slots=None, offsets=No
         h.ldr = _rows(residual, "residual", (X.dtype,), shape)
     pre = torch.empty(shape, dtype=X.dtype, device=X.device) if with_pre else None
     dev = _one_device(X, W, bias, residual, slots, offsets, Y)
-    with torch.cuda.device(dev):
-        need = load().fk_linear_workspace_size(ctypes.byref(h), 0) or 256
-        p, n = _workspace(need, dev, workspace)
-        _check(load().fk_linear(ctypes.byref(h), _ptr(X), _ptr(W), _ptr(bias), _ptr(residual), _ptr(slots),
-                                _ptr(offsets), _ptr(Y), _ptr(pre), ctypes.c_void_p(p), ctypes.c_size_t(n),
-                                _stream(dev)))
+    need = load().fk_linear_workspace_size(ctypes.byref(h), 0) or 256
+    p, n = _scratch(need, dev, workspace)
+    _run(load().fk_linear, dev, ctypes.byref(h), _at(X), _at(W), _at(bias), _at(residual), _at(slots), _at(offsets),
+         _at(Y), _at(pre), p, n)
     return Y, pre
 
 
@@ -737,15 +765,13 @@ def fk_linear_backward(dY, X, W, act="none", pre=None, slots=None, offsets=None,
         raise ValueError(f"bias_dtype must be {X.dtype} or torch.float32")
     h.bias_dtype = DTYPES[bias_dtype]
     dev = _one_device(dY, X, W, pre, slots, offsets)
-    dX = torch.empty((h.M, h.K), dtype=X.dtype, device=dev) if with_dx else None
-    dW = torch.empty(W.shape, dtype=X.dtype, device=dev) if with_dw else None
-    db = torch.empty(W.shape[:-1], dtype=bias_dtype, device=dev) if with_bias else None
-    with torch.cuda.device(dev):
-        need = load().fk_linear_workspace_size(ctypes.byref(h), 1) or 256
-        p, n = _workspace(need, dev, workspace)
-        _check(load().fk_linear_backward(ctypes.byref(h), _ptr(dY), _ptr(X), _ptr(W), _ptr(pre), _ptr(slots),
-                                         _ptr(offsets), _ptr(dX), _ptr(dW), _ptr(db), ctypes.c_void_p(p),
-                                         ctypes.c_size_t(n), _stream(dev)))
+    dX = torch.empty((h.M, h.K), dtype=X.dtype, device=X.device) if with_dx else None
+    dW = torch.empty(W.shape, dtype=X.dtype, device=X.device) if with_dw else None
+    db = torch.empty(W.shape[:-1], dtype=bias_dtype, device=X.device) if with_bias else None
+    need = load().fk_linear_workspace_size(ctypes.byref(h), 1) or 256
+    p, n = _scratch(need, dev, workspace)
+    _run(load().fk_linear_backward, dev, ctypes.byref(h), _at(dY), _at(X), _at(W), _at(pre), _at(slots), _at(offsets),
+         _at(dX), _at(dW), _at(db), p, n)
     return dX, dW, db
 
 
@@ -768,12 +794,11 @@ def fk_combine(Y, k: int, gates=None, residual=None, out=None):
     _gates_of(gates, rows, k)
     ldr = _rows(residual, "residual", (Y.dtype,), (rows, d)) if residual is not None else d
     if out is None:
-        out = torch.empty((rows, d), dtype=Y.dtype, device=Y.device)
-    ldo = _rows(out, "out", (Y.dtype,), (rows, d))
+        out, ldo = torch.empty((rows, d), dtype=Y.dtype, device=Y.device), d
+    else:
+        ldo = _rows(out, "out", (Y.dtype,), (rows, d))
     dev = _one_device(Y, gates, residual, out)
-    with torch.cuda.device(dev):
-        _check(load().fk_combine(DTYPES[Y.dtype], _ptr(Y), rows, k, d, _ptr(gates), _ptr(residual), ldr, _ptr(out),
-                                 ldo, _stream(dev)))
+    _run(load().fk_combine, dev, DTYPES[Y.dtype], _at(Y), rows, k, d, _at(gates), _at(residual), ldr, _at(out), ldo)
     return out
 
 
@@ -787,11 +812,10 @@ def fk_combine_backward(dOut, Y, gates):
     k = gates.shape[1]
     _dev(Y, "Y", dOut.dtype, (rows * k, d))
     dev = _one_device(dOut, Y, gates)
-    dY = torch.empty((rows * k, d), dtype=dOut.dtype, device=dev)
-    dgates = torch.empty((rows, k), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(load().fk_combine_backward(DTYPES[dOut.dtype], _ptr(dOut), ldo, _ptr(Y), rows, k, d, _ptr(gates),
-                                          _ptr(dY), _ptr(dgates), _stream(dev)))
+    dY = torch.empty((rows * k, d), dtype=dOut.dtype, device=dOut.device)
+    dgates = torch.empty((rows, k), dtype=torch.float32, device=dOut.device)
+    _run(load().fk_combine_backward, dev, DTYPES[dOut.dtype], _at(dOut), ldo, _at(Y), rows, k, d, _at(gates), _at(dY),
+         _at(dgates))
     return dY, dgates
 
 
