@@ -596,10 +596,13 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     int64_t kbeg = 0, ka = a.ka, kb = a.kb;
     int64_t pos = 0;         // kDw: the group's first position
     if constexpr (KIND == kDw) {
-        const int64_t per = mtiles * ntiles;
-        const int64_t id = xcd_tile(blockIdx.x, per * a.G);
-        t.g = (int)(id / per);
-        const int64_t in = id % per;
+        // every XCD takes a run of every group's tiles: groups differ in the
+        // length of their sums, so runs of whole groups would not be even
+        const int64_t per = mtiles * ntiles, run = (per + 7) >> 3;
+        const int64_t i = blockIdx.x >> 3;
+        t.g = (int)(i / run);
+        const int64_t in = (blockIdx.x & 7) * run + i % run;
+        if (in >= per) return;
         nt = in % ntiles;
         r0 = in / ntiles * BM;
         nrows = a.rows - r0 < BM ? a.rows - r0 : BM;
@@ -1283,7 +1286,7 @@ hipError_t run_product(LinArgs a, int tile, hipStream_t s) {
     int64_t mt, grid;
     if (KIND == kDw) {
         mt = cdiv(a.rows, tile);
-        grid = mt * nt * a.G;
+        grid = (mt * nt + 7) / 8 * 8 * a.G;
     } else if (a.offsets == nullptr) {
         mt = cdiv(a.rows, tile);
         grid = mt * nt;
