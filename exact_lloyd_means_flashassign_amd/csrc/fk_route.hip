@@ -251,8 +251,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) float sm[];
     const int lane = threadIdx.x % LPR;
     const int col = lane * VPL;
-    int *counts = reinterpret_cast<int *>(sm) + COLS;
-    for (int i = threadIdx.x; i < 2 * COLS; i += kRouteThreads) sm[i] = 0.0f;  // (0 as an integer too)
+    int *counts = reinterpret_cast<int *>(sm) + kRouteThreads / 64 * COLS;
+    for (int i = threadIdx.x; i < COLS; i += kRouteThreads) counts[i] = 0;
     __syncthreads();
     float psum[VPL];
 #pragma unroll
@@ -355,31 +355,31 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     const int wv = threadIdx.x >> 6;
     __shared__ float s_z[WV];
     __shared__ int s_live[WV];
-    for (int w = 0; w < WV; ++w) {
-        if (w == wv) {
-            if ((threadIdx.x & 63) < LPR) {
+    // sm: each wave's sums, then the counts
+    if ((threadIdx.x & 63) < LPR) {
 #pragma unroll
-                for (int v = 0; v < VPL; ++v) sm[col + v] += psum[v];
-            }
-            if ((threadIdx.x & 63) == 0) {
-                s_z[w] = zsum;
-                s_live[w] = nlive;
-            }
-        }
-        __syncthreads();
+        for (int v = 0; v < VPL; ++v) sm[wv * COLS + col + v] = psum[v];
     }
+    if ((threadIdx.x & 63) == 0) {
+        s_z[wv] = zsum;
+        s_live[wv] = nlive;
+    }
+    __syncthreads();
     const int F = part_floats(a.E);
     float *out = a.part + (size_t)blockIdx.x * 2 * F;
     for (int c = threadIdx.x; c < F; c += kRouteThreads) {
         float z = 0.0f;
         int n = 0;
-        if (c == a.E) {
+        if (c < a.E) {
+#pragma unroll
+            for (int w = 0; w < WV; ++w) z += sm[w * COLS + c];
+        } else if (c == a.E) {
             for (int w = 0; w < WV; ++w) {
                 z += s_z[w];
                 n += s_live[w];
             }
         }
-        out[c] = c < a.E ? sm[c] : z;
+        out[c] = z;
         out[F + c] = __int_as_float(c < a.E ? counts[c] : n);
     }
     if (gridDim.x == 1) {
@@ -509,9 +509,9 @@ template <typename T, bool BWD>
 hipError_t dispatch_route(const RouteArgs &a, hipStream_t s) {
     const int lpr = lanes_per_row(a.E);
     const int vpl = a.E > 512 ? 16 : 8;
-    // the sums and counts of every column; the finish's runs and totals
+    // the waves' sums and the counts of every column; the finish's runs and totals
     const int row = part_row(a.E), runs = kRouteThreads / (row / 4);
-    const size_t need = (size_t)(runs + 1) * row * 4, cols = (size_t)lpr * vpl * 8;
+    const size_t need = (size_t)(runs + 1) * row * 4, cols = (size_t)lpr * vpl * 4 * (kRouteThreads / 64 + 1);
     const size_t lds = need > cols ? need : cols;
     const int64_t per = 256 / lpr;
     const unsigned bgrid = (unsigned)(cdiv(a.T, per) < 4096 ? cdiv(a.T, per) : 4096);
