@@ -504,7 +504,16 @@ struct Epilogue {
     // group), below 0: none.  SURE: every row and column exists, on whole chunks.
     // SURE comes with the residual's chunks, which were sent for earlier.
     struct Eight {
-        Chunk<T, 16 / (int)sizeof(T)> c[sizeof(T) / 2];
+        static constexpr int E = 16 / (int)sizeof(T);
+        Chunk<T, E> c[8 / E];
+        __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+            for (int i = 0; i < 8 / E; ++i) c[i].load(p + i * E);
+        }
+        __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (float)c[i / E].e[i % E];
+        }
     };
     template <bool SURE, int N>
     __device__ __forceinline__ void out(const LinArgs &a, int g, const int64_t (&crow)[N], float (&v)[N * 8],
@@ -515,8 +524,7 @@ struct Epilogue {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 if (SURE) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) r[k][i] = (float)res[k].c[i * (int)sizeof(T) / 16].e[i % (16 / (int)sizeof(T))];
+                    res[k].values(r[k]);
                 } else if (crow[k] >= 0) {
                     get((const T *)a.R + crow[k] * a.ldr + col, r[k], n);
                 }
@@ -922,9 +930,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     auto send_for = [&](int p, int q) {
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const T *from = (const T *)a.R + row_at(p, q, k) * a.ldr + col;
-#pragma unroll
-            for (int c = 0; c < (int)sizeof(T) / 2; ++c) res[k].c[c].load(from + c * E);
+            res[k].load((const T *)a.R + row_at(p, q, k) * a.ldr + col);
         }
     };
     // the tiles are read to the end, and no load to LDS is under way
@@ -1170,25 +1176,31 @@ __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int
     const int n = a.N - col >= 8 ? 8 : (a.N > col ? (int)(a.N - col) : 0);
     const int npad = lddz - col >= 8 ? 8 : (lddz > col ? (int)(lddz - col) : 0);
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (n > 0 || (dZ != nullptr && npad > 0)) {
+    // SURE: all rows and columns of the tile exist, on whole chunks.  One row of
+    // the thread's eight at a time: several together cost waves, and with them
+    // time (32768 x 4096: one 251 us with a thin dX, four 265).
+    auto rows = [&](auto sure) {
+        constexpr bool SURE = decltype(sure)::value;
+#pragma unroll 1
         for (int64_t p = t.p0 + ry; p < t.p1; p += 8) {
             const int64_t row = a.cmap(p);
-            float d[8];
-            if (df32) Epilogue<float>::get((const float *)dY + row * ldd + col, d, n);
-            else Epilogue<T>::get((const T *)dY + row * ldd + col, d, n);
+            float d[8], z[8];
+            if (df32) Epilogue<float>::template get<SURE>((const float *)dY + row * ldd + col, d, n);
+            else Epilogue<T>::template get<SURE>((const T *)dY + row * ldd + col, d, n);
             if (a.act != FK_ACT_NONE) {
-                float z[8];
-                Epilogue<T>::get((const T *)a.Z + row * a.ldz + col, z, n);
+                Epilogue<T>::template get<SURE>((const T *)a.Z + row * a.ldz + col, z, n);
                 times_slope(a.act, z, d);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                d[i] = i < n ? d[i] : 0.0f;
+                d[i] = SURE || i < n ? d[i] : 0.0f;
                 s[i] += d[i];
             }
-            if (dZ != nullptr) Epilogue<T>::put(dZ + p * lddz + col, d, npad);
+            if (dZ != nullptr) Epilogue<T>::template put<SURE>(dZ + p * lddz + col, d, npad);
         }
-    }
+    };
+    if (a.chunked && t.p1 - t.p0 == kGradRows && (int64_t)(blockIdx.y + 1) * 256 <= a.N) rows(std::true_type{});
+    else if (n > 0 || (dZ != nullptr && npad > 0)) rows(std::false_type{});
     if (colsum == nullptr) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sm[ry][cx * 8 + i] = s[i];
@@ -1469,6 +1481,7 @@ hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     LinArgs c{};
     c.offsets = b.offsets, c.cmap = row_map(b.slots, h.M, 1), c.M = h.M, c.N = h.N, c.G = G, c.act = h.act;
     c.Z = (void *)b.Zin, c.ldz = h.ldz;
+    c.chunked = on_chunks(b.dY, h.ldy, dtype_size(h.ydtype)) && on_chunks(b.Zin, h.ldz, sizeof(T));
     if ((p.make_dz && (b.dX || b.dW)) || b.db) {
         T *dz = p.make_dz && (b.dX || b.dW) ? (T *)(ws + p.dz) : nullptr;
         float *cs = b.db ? (float *)(ws + p.colsum) : nullptr;
