@@ -1214,9 +1214,11 @@ __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int
     }
 }
 
-// db of one group: its row tiles' column sums in order, 16 threads down a column
+// db of one group: its row tiles' column sums in order, 16 threads down a
+// column.  There are `most` row tiles at most; offsets that do not rise cannot
+// reach past them.
 template <typename T>
-__global__ __launch_bounds__(256) void k_bias_grad(LinArgs a, const float *colsum, void *db, int f32) {
+__global__ __launch_bounds__(256) void k_bias_grad(LinArgs a, const float *colsum, int64_t most, void *db, int f32) {
     __shared__ float sm[16][17];
     __shared__ int64_t range[2];
     const int g = blockIdx.y;
@@ -1239,7 +1241,7 @@ __global__ __launch_bounds__(256) void k_bias_grad(LinArgs a, const float *colsu
         }
         if (threadIdx.x == 0) {
             range[0] = first;
-            range[1] = first + tiles;
+            range[1] = first + tiles < most ? first + tiles : most;
         }
     }
     __syncthreads();
@@ -1490,7 +1492,7 @@ hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
                 c, b.dY, h.ldy, h.ydtype == FK_F32, dz, np, cs);
         }
         if (b.db)
-            k_bias_grad<T><<<dim3((unsigned)cdiv(h.N, 16), (unsigned)G), 256, 0, s>>>(c, cs, b.db, h.bias_f32);
+            k_bias_grad<T><<<dim3((unsigned)cdiv(h.N, 16), (unsigned)G), 256, 0, s>>>(c, cs, p.grad_tiles, b.db, h.bias_f32);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const void *X = b.X, *W = b.W;
