@@ -1067,17 +1067,22 @@ __global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
 
 // ---- a few rows against a whole weight matrix -----------------------------------------
 //
-// Bound by the stream of the weights.  A workgroup takes 16 rows of W (columns
-// of C); its waves take every WV-th 128-byte stretch of the sum each and read W
-// straight into the matrix instruction's registers, 16 bytes a lane, eight
-// stretches' halves in flight; the rows of X come from cache.  The waves'
-// sums are added in wave order through LDS.  Groups of more than 16 MT rows
-// are left to the tiled product (dense: there are none).
-template <typename T, int MT, int WV, bool WIDE>
+// Up to 16 rows, those that one matrix instruction takes.  Bound by the stream
+// of the weights.  A workgroup takes NT blocks of 16 rows of W (columns of C);
+// its waves take every WV-th run of U steps of the sum and read W straight into
+// the matrix instruction's registers, 16 bytes a lane, all loads of a run in
+// flight; the rows of X come from cache, and rows that do not exist are not
+// read.  The waves' sums are added in wave order through LDS.  Groups of more
+// rows are left to the tiled product.
+//
+// bf16, weights from memory: one row by 16384 x 4096 28 us (4.8 TB/s; the
+// tiled product 40), 16 rows 35 us (40); 16 rows by 4096 x 4096 13 us (18).
+// More blocks of rows or 8 waves gained nothing.
+template <typename T, int NT, int WV, bool WIDE>
 __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int STEP = 4 * E;  // elements of the sum in one load of a wave
-    __shared__ float sm[WV][MT * 16][17];
+    __shared__ float sm[WV][16][NT * 16 + 1];
     const int g = blockIdx.y;
     int64_t p0 = 0, cnt = a.M;
     if (a.offsets != nullptr) {
@@ -1087,19 +1092,18 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l = lane & 15, q = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int64_t n = n0 + l < a.N ? n0 + l : a.N - 1;
-    const T *w = (const T *)a.B + (int64_t)g * a.gsb + n * a.ldb;
-    const T *x[MT];
-    bool xin[MT];
+    const int64_t n0 = (int64_t)blockIdx.x * (NT * 16);
+    const T *w[NT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        xin[t] = t * 16 + l < cnt;
-        x[t] = (const T *)a.A + a.amap(p0 + (xin[t] ? t * 16 + l : 0)) * a.lda;
+    for (int t = 0; t < NT; ++t) {
+        const int64_t n = n0 + t * 16 + l;
+        w[t] = (const T *)a.B + (int64_t)g * a.gsb + (n < a.N ? n : a.N - 1) * a.ldb;
     }
-    v4f acc[MT];
+    const bool xin = l < cnt;
+    const T *x = (const T *)a.A + a.amap(p0 + (xin ? l : 0)) * a.lda;
+    v4f acc[NT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < NT; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     typedef typename Mma<T>::Frag Frag;
     const int K = (int)a.ka;
     auto load = [&](const T *p, int k, bool in) {
@@ -1115,28 +1119,28 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
         }
         return f;
     };
-    constexpr int U = 4;  // loads of W a wave has in flight
+    constexpr int U = 4;  // steps of the sum a wave has in flight
     for (int k0 = wave * STEP * U; k0 < K; k0 += WV * STEP * U) {
-        Frag fw[U], fx[U][MT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) fw[u] = load(w, k0 + u * STEP + q * E, true);
+        Frag fw[U][NT], fx[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int t = 0; t < MT; ++t) fx[u][t] = load(x[t], k0 + u * STEP + q * E, xin[t]);
+            for (int j = 0; j < NT; ++j) fw[u][j] = load(w[j], k0 + u * STEP + q * E, true);
+#pragma unroll
+        for (int u = 0; u < U; ++u) fx[u] = load(x, k0 + u * STEP + q * E, xin);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int t = 0; t < MT; ++t) acc[t] = Mma<T>::m16(fw[u], fx[u][t], acc[t]);
+            for (int j = 0; j < NT; ++j) acc[j] = Mma<T>::m16(fw[u][j], fx[u], acc[j]);
     }
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sm[wave][t * 16 + l][q * 4 + i] = acc[t][i];
+        for (int i = 0; i < 4; ++i) sm[wave][l][j * 16 + q * 4 + i] = acc[j][i];
     __syncthreads();
     // 8 columns a thread
-    for (int i = threadIdx.x; i < MT * 32; i += WV * 64) {
-        const int m = i >> 1, c = (i & 1) * 8;
+    for (int i = threadIdx.x; i < 16 * NT * 2; i += WV * 64) {
+        const int m = i / (NT * 2), c = i % (NT * 2) * 8;
         if (m >= cnt) continue;
         float v[8];
 #pragma unroll
@@ -1284,7 +1288,7 @@ __global__ __launch_bounds__(256) void k_pad_rows(const T *in, int64_t ldi, RowM
 
 // ---- host ---------------------------------------------------------------------------------
 
-constexpr int kFewRows = 16;      // most rows of a group that k_product_few takes
+constexpr int kFewRows = 16;  // most rows of a group that k_product_few takes
 constexpr int kCus = 256;
 
 // Whether eight columns from a multiple of eight on are whole 16-byte chunks.
@@ -1327,23 +1331,52 @@ hipError_t run_product(LinArgs a, int tile, hipStream_t s) {
 
 template <typename T, bool WIDE>
 hipError_t run_few(const LinArgs &a, hipStream_t s) {
-    const dim3 gr((unsigned)cdiv(a.N, 16), (unsigned)(a.offsets ? a.G : 1));
-    k_product_few<T, 1, 4, WIDE><<<gr, 256, 0, s>>>(a);
+    // 32 columns a workgroup where there are many of them.  bf16: 64 groups of
+    // 1 to 16 rows of 4096 x 2048, 8 on average: 205 us against 231 with 16
+    // columns; one row by 16384 x 4096 (1024 workgroups of 16): 38 against 28.
+    const int groups = a.offsets ? a.G : 1;
+    if (cdiv(a.N, 16) * groups >= 4096) {
+        k_product_few<T, 2, 4, WIDE><<<dim3((unsigned)cdiv(a.N, 32), (unsigned)groups), 256, 0, s>>>(a);
+    } else {
+        k_product_few<T, 1, 4, WIDE><<<dim3((unsigned)cdiv(a.N, 16), (unsigned)groups), 256, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
-// Tile and splits of a product with `mt` x `nt` x `groups` tiles of 256 and a
-// sum of `steps` 128-byte steps.
+// Tile and splits of a product of `groups` matrices of rows x cols with sums
+// of `steps` 128-byte steps.
+//
+// Tiles of 256 read half as much a product as those of 128 and run at 1350
+// TFLOP/s where those reach 1100 (bf16, 16384 x 8192 x 4096), if there are
+// enough of them: on 256 CUs, 160 tiles of 256 took 80, 78 and 87 us (forward,
+// dX and dW, 4096 x 2560 x 4096) against 88, 85 and 114 for four times as many
+// of 128; 128 tiles of 256 took 84, 67 and 86 against 70, 75 and 84.
+//
+// A sum is split where the tiles leave CUs without work.  In units of a step's
+// time in bf16 (about 0.4 us with a workgroup a CU): the join's launch costs 8,
+// its partial tiles, written and read, 1/8 each; fp32's steps take four times
+// as long and more, and those of a single row tile, whose other operand comes
+// from memory, twice (32 rows by 16384 x 4096, 128 tiles of 64 steps: 45 us,
+// in two splits 41).  Measured in bf16 with 1, 2, 4 and 8 splits (us): 32 tiles
+// of 64 steps 27, 21, 19, 22; 64 tiles of 64 steps 28, 24, 28, 32; 128 tiles of
+// 64 steps 30, 34 (two), 64 tiles of 256 steps 92, 61, 55, 64; 64 tiles of 32
+// steps 16, 19, 22, 28.
 struct Shape {
     int tile, splits;
 };
-Shape pick_shape(int64_t rows, int64_t cols, int64_t groups, int64_t steps) {
+Shape pick_shape(int64_t rows, int64_t cols, int64_t groups, int64_t steps, int dtype) {
     Shape s;
     const int64_t big = cdiv(rows, 256) * cdiv(cols, 256) * groups;
-    s.tile = rows > 128 && big >= kCus * 3 / 4 ? 256 : 128;
-    const int64_t tiles = cdiv(rows, s.tile) * cdiv(cols, s.tile) * groups;
+    s.tile = rows > 128 && big >= kCus * 5 / 8 ? 256 : 128;
     s.splits = 1;
-    while (s.tile == 128 && s.splits < 16 && tiles * s.splits * 2 <= kCus && steps / (s.splits * 2) >= 4) s.splits *= 2;
+    if (s.tile == 256) return s;
+    const int64_t tiles = cdiv(rows, 128) * cdiv(cols, 128) * groups;
+    const int64_t unit = dtype == FK_F32 ? 4 : rows <= 128 ? 2 : 1;
+    int64_t best = 8 * steps * unit;  // (in eighths)
+    for (int n = 2; n <= 16 && n <= steps && tiles * n <= kCus; n *= 2) {
+        const int64_t cost = 8 * cdiv(steps, n) * unit + 64 + tiles * n;
+        if (cost < best) best = cost, s.splits = n;
+    }
     return s;
 }
 
@@ -1384,7 +1417,10 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
         off += align_up(bytes > 0 ? bytes : 1, 256);
         return o;
     };
-    p.few = !backward && mean <= kFewRows;
+    // in groups only where few are likely to be left to the tiled product, which
+    // then runs too: 64 groups of 4096 x 2048 with 8 rows on average 205 us (the
+    // tiled product alone 214), with 16 on average 235 (217)
+    p.few = !backward && mean <= (h.grouped ? kFewRows / 2 : kFewRows);
     p.tiled = backward || h.grouped || !p.few;
     const int64_t kp = cdiv(h.K, bk / 8) * (bk / 8);
     p.pad_x = p.tiled && !readable(h.K, h.ldx, h.dtype);
@@ -1396,7 +1432,7 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
     if (p.pad_x) p.xpad = take(pad16(p.sort_x ? h.M : h.M / h.share, h.K, h.dtype));
     if (p.pad_w) p.wpad = take(pad16(wrows, h.K, h.dtype));
     if (!backward) {
-        const Shape s = pick_shape(h.grouped ? mean : h.M, h.N, groups, cdiv(h.K, bk));
+        const Shape s = pick_shape(h.grouped ? mean : h.M, h.N, groups, cdiv(h.K, bk), h.dtype);
         p.tile = s.tile, p.splits = s.splits;
         if (p.tiled && p.splits > 1) p.part = take((size_t)p.splits * h.M * h.N * 4);
         p.total = off > 0 ? off : 256;
@@ -1408,8 +1444,8 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
     if (p.make_dz) p.dz = take(pad16(h.M, h.N, h.dtype));
     p.grad_tiles = h.grouped ? h.M / kGradRows + (h.G < h.M ? h.G : h.M) : cdiv(h.M, kGradRows);
     p.colsum = take((size_t)p.grad_tiles * h.N * 4);
-    const Shape sx = pick_shape(h.grouped ? mean : h.M, h.K, groups, cdiv(h.N, bk));
-    const Shape sw = pick_shape(h.N, h.K, groups, cdiv(mean, bk));
+    const Shape sx = pick_shape(h.grouped ? mean : h.M, h.K, groups, cdiv(h.N, bk), h.dtype);
+    const Shape sw = pick_shape(h.N, h.K, groups, cdiv(mean, bk), h.dtype);
     p.tile = sx.tile, p.splits = sx.splits, p.tile_w = sw.tile, p.splits_w = sw.splits;
     const size_t px = p.splits > 1 ? (size_t)p.splits * h.M * h.K * 4 : 0;
     const size_t pw = p.splits_w > 1 ? (size_t)p.splits_w * wrows * h.K * 4 : 0;
