@@ -801,7 +801,9 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
             read_b(0, place_b(0, 0), n);
         }
         landed(std::integral_constant<int, 4 * IT>{});
-        // two tiles a round; of an odd number the last one's partner is zeros
+        // two tiles a round; of an odd number the last one's partner is zeros,
+        // multiplied all the same with tiles of 256, whose registers the branch
+        // would spill
         const int64_t whole = (ea < eb ? ea : eb) - kbeg;  // steps of the sum in both
         int64_t i = 0;
         for (; (i + 4) * BK <= whole; i += 2) {
@@ -810,7 +812,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         }
         for (; i < steps; i += 2) {
             tile(c0_, std::true_type{}, i);
-            tile(c1_, std::true_type{}, i + 1);
+            if (BS == 256 || i + 1 < steps) tile(c1_, std::true_type{}, i + 1);
         }
     }
     const int lane = threadIdx.x & 63;
@@ -1270,19 +1272,30 @@ __global__ __launch_bounds__(256) void k_bias_grad(LinArgs a, const float *colsu
 
 // out[r] = in[map(r)] with its columns padded by zeros to ldo (whole chunks): the
 // tiled product reads 16 bytes at a time, so operands whose rows do not start
-// on 16 bytes are laid out once more first.
+// on 16 bytes are laid out once more first, both of a product in one launch.
+// 2^lx lanes across a row's chunks.
+struct PadJob {
+    const void *in;
+    void *out;
+    RowMap map;
+    int64_t rows, ldi, ldo;
+    int cols, lx;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void k_pad_rows(const T *in, int64_t ldi, RowMap map, int64_t rows, int64_t cols,
-                                                  T *out, int64_t ldo) {
+__global__ __launch_bounds__(256) void k_pad_rows(PadJob j0, PadJob j1) {
     constexpr int E = 16 / (int)sizeof(T);
-    const int64_t chunks = ldo / E;
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < rows * chunks; id += (int64_t)gridDim.x * 256) {
-        const int64_t r = id / chunks, c = id % chunks * E;
-        const T *p = in + map(r) * ldi + c;
-        Chunk<T, E> o;
+    const PadJob j = blockIdx.y ? j1 : j0;
+    const int tx = threadIdx.x & ((1 << j.lx) - 1), ty = threadIdx.x >> j.lx;
+    const int rpb = 256 >> j.lx;
+    for (int64_t r = (int64_t)blockIdx.x * rpb + ty; r < j.rows; r += (int64_t)gridDim.x * rpb) {
+        const T *p = (const T *)j.in + j.map(r) * j.ldi;
+        T *q = (T *)j.out + r * j.ldo;
+        for (int64_t c = (int64_t)tx * E; c < j.ldo; c += (int64_t)E << j.lx) {
+            Chunk<T, E> o;
 #pragma unroll
-        for (int i = 0; i < E; ++i) o.e[i] = c + i < cols ? p[i] : (T)0.0f;
-        o.store(out + r * ldo + c);
+            for (int i = 0; i < E; ++i) o.e[i] = c + i < j.cols ? p[c + i] : (T)0.0f;
+            o.store(q + c);
+        }
     }
 }
 
@@ -1457,19 +1470,33 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
 namespace {
 
 template <typename T>
-hipError_t pad_rows(const void *in, int64_t ldi, const RowMap &map, int64_t rows, int64_t cols, void *out, hipStream_t s) {
+PadJob pad_job(const void *in, int64_t ldi, const RowMap &map, int64_t rows, int64_t cols, void *out) {
     constexpr int E = 16 / (int)sizeof(T);
-    const int64_t ldo = cdiv(cols, E) * E;
-    const int64_t n = cdiv(rows * (ldo / E), 256);
-    if (n > 0) k_pad_rows<T><<<(unsigned)(n < 65536 ? n : 65536), 256, 0, s>>>((const T *)in, ldi, map, rows, cols, (T *)out, ldo);
-    return hipGetLastError();
+    PadJob j{in, out, map, rows, ldi, cdiv(cols, E) * E, (int)cols, 0};
+    while (j.lx < 8 && (1 << j.lx) < cdiv(cols, E)) ++j.lx;
+    return j;
 }
 
-// X with padded rows, or in position order (sort_x)
+// X with padded rows, or in position order (sort_x), and W with padded rows,
+// those of them that the plan and `x`, `w` ask for
 template <typename T>
-hipError_t lay_out_x(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, char *ws, hipStream_t s) {
-    const RowMap map = p.sort_x ? row_map(b.slots, h.M, h.share) : row_map(nullptr, h.M, 1);
-    return pad_rows<T>(b.X, h.ldx, map, p.sort_x ? h.M : h.M / h.share, h.K, ws + p.xpad, s);
+hipError_t lay_out(const LinearShape &h, const LinearPlan &p, const LinearBufs &b, bool x, bool w, char *ws,
+                   hipStream_t s) {
+    PadJob j[2];
+    int n = 0;
+    if (p.pad_x && x) {
+        const RowMap map = p.sort_x ? row_map(b.slots, h.M, h.share) : row_map(nullptr, h.M, 1);
+        j[n++] = pad_job<T>(b.X, h.ldx, map, p.sort_x ? h.M : h.M / h.share, h.K, ws + p.xpad);
+    }
+    if (p.pad_w && w) j[n++] = pad_job<T>(b.W, h.ldw, row_map(nullptr, h.M, 1), (h.grouped ? h.G : 1) * h.N, h.K, ws + p.wpad);
+    int64_t blocks = 0;
+    for (int i = 0; i < n; ++i) {
+        const int64_t need = cdiv(j[i].rows, 256 >> j[i].lx);
+        if (need > blocks) blocks = need;
+    }
+    if (blocks > 0)
+        k_pad_rows<T><<<dim3((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)n), 256, 0, s>>>(j[0], j[n - 1]);
+    return hipGetLastError();
 }
 
 template <typename T>
@@ -1484,7 +1511,6 @@ hipError_t linear_fwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     a.offsets = b.offsets;
     a.amap = row_map(b.slots, h.M, h.share);
     a.cmap = row_map(b.slots, h.M, 1);
-    const RowMap plain = row_map(nullptr, h.M, 1);
     a.M = a.rows = h.M, a.N = h.N, a.G = h.grouped ? h.G : 1, a.act = h.act, a.splits = p.splits;
     a.part = (float *)(ws + p.part);
     hipError_t e = hipSuccess;
@@ -1497,16 +1523,12 @@ hipError_t linear_fwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     a.skip = p.few ? kFewRows : 0;
     a.A = b.X, a.lda = h.ldx, a.B = b.W, a.ldb = h.ldw, a.gsb = h.N * h.ldw;
     a.ka = a.kb = kp;
+    if ((e = lay_out<T>(h, p, b, true, true, ws, s)) != hipSuccess) return e;
     if (p.pad_x) {
-        if ((e = lay_out_x<T>(h, p, b, ws, s)) != hipSuccess) return e;
         a.A = ws + p.xpad, a.lda = kp;
-        if (p.sort_x) a.amap = plain;
+        if (p.sort_x) a.amap = row_map(nullptr, h.M, 1);
     }
-    if (p.pad_w) {
-        e = pad_rows<T>(b.W, h.ldw, plain, a.G * h.N, h.K, ws + p.wpad, s);
-        if (e != hipSuccess) return e;
-        a.B = ws + p.wpad, a.ldb = kp, a.gsb = h.N * kp;
-    }
+    if (p.pad_w) a.B = ws + p.wpad, a.ldb = kp, a.gsb = h.N * kp;
     return run_product<T, kFwd>(a, p.tile, s);
 }
 
@@ -1533,14 +1555,9 @@ hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
     }
     const void *X = b.X, *W = b.W;
     int64_t ldx = h.ldx, ldw = h.ldw;
-    if (p.pad_x && b.dW) {
-        if ((e = lay_out_x<T>(h, p, b, ws, s)) != hipSuccess) return e;
-        X = ws + p.xpad, ldx = kp;
-    }
-    if (p.pad_w && b.dX) {
-        if ((e = pad_rows<T>(W, ldw, row_map(nullptr, h.M, 1), G * h.N, h.K, ws + p.wpad, s)) != hipSuccess) return e;
-        W = ws + p.wpad, ldw = kp;
-    }
+    if ((e = lay_out<T>(h, p, b, b.dW != nullptr, b.dX != nullptr, ws, s)) != hipSuccess) return e;
+    if (p.pad_x) X = ws + p.xpad, ldx = kp;
+    if (p.pad_w) W = ws + p.wpad, ldw = kp;
     LinArgs a{};
     a.offsets = b.offsets, a.M = h.M, a.G = G, a.act = FK_ACT_NONE, a.part = (float *)(ws + p.part);
     a.A = p.make_dz ? ws + p.dz : b.dY;
