@@ -7,6 +7,14 @@
 // p runs over the positions of a slot list sorted by group: slot(p) =
 // slots[p], row(p) = slots[p] / share, and group g owns [offsets[g],
 // offsets[g+1]).  A plain product has one group and slot(p) = row(p) = p.
+//
+// Sums are fp32 in the matrix instructions' accumulators; bias, activation and
+// residual are applied to them, and each output is rounded once.  dZ is
+// rounded to the operands' type before it is multiplied, as the 16-bit matrix
+// instructions need; db is the sum of the unrounded values.  Three kernels
+// share the work: tiles (k_product), which are bound by the matrix units; a few
+// rows (k_product_few), bound by the stream of the weights; and the
+// element-wise step of the gradients (k_act_grad), bound by memory.
 #include <type_traits>
 
 #include "fk.h"
@@ -576,6 +584,15 @@ struct Epilogue {
 // spread evenly over the products and have most of two tiles' time to arrive.
 // One wave a SIMD holds 128 x 128 of C in 256 accumulation registers: 8 waves
 // of 128 x 64 read 1.5 times as much from LDS.
+//
+// Measured in bf16 at 16384 x 8192 x 4096: forward 780 to 810 us (1360 to 1410
+// TFLOP/s), dX 815, dW 780 to 795, where the library's product takes 743
+// (1480); with gelu and a residual in the epilogue the
+// forward pass takes 960.  In the loop the matrix units are busy 77 % of the
+// time (the loads' issue costs about 12 %), and a workgroup's first loads and last stores, which nothing overlaps with one
+// workgroup a CU, about 15 us of its 100.  In fp32 tiles of 128 reach 145
+// TFLOP/s (4096 x 1024 x 4096, the library 149) where the tiles divide the CUs
+// evenly, and 63 where they do not (5003 x 1001 x 769: 320 tiles on 256 CUs).
 template <typename T, int KIND, int BS>
 __global__ __launch_bounds__(kTileThreads)
 __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void k_product(LinArgs a, int64_t mtiles,
@@ -1163,6 +1180,8 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
 // that the matrix instructions take (and padded with zeros to whole chunks),
 // and the partial column sums of the unrounded values for db: one row tile of
 // one group and 8 columns a thread.
+//
+// Bound by memory: 16384 x 4096 in bf16 with gelu_tanh 86 us (4.7 TB/s).
 constexpr int kGradRows = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int64_t ldd, int df32, T *dZ, int64_t lddz,

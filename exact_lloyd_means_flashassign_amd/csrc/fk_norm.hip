@@ -15,6 +15,10 @@
 // for each workgroup and are added in a fixed order by a second kernel, so
 // there are no atomics and results are bitwise reproducible.  All sums are
 // fp32.
+//
+// Measured at 32749 x 4096 in bf16: forward 97 us (5.5 TB/s), backward 157 us
+// (5.1 TB/s) and 7 us for the partial rows, where a copy of 1 GiB runs at 5.1.
+// A few rows take 4 us on the device, less than the launch.
 #include "fk.h"
 #include "fk_block.h"
 #include "fk_internal.h"

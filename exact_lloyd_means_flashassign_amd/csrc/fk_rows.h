@@ -13,21 +13,6 @@ namespace fk {
 inline bool known_dtype(int32_t t) { return t == FK_F32 || t == FK_BF16 || t == FK_F16; }
 inline size_t dtype_size(int32_t t) { return t == FK_F32 ? 4 : 2; }
 
-template <typename T>
-struct ElemOf;
-template <>
-struct ElemOf<float> {
-    static constexpr int code = FK_F32;
-};
-template <>
-struct ElemOf<__bf16> {
-    static constexpr int code = FK_BF16;
-};
-template <>
-struct ElemOf<_Float16> {
-    static constexpr int code = FK_F16;
-};
-
 // V consecutive elements (V = 1, or as many as 16 bytes hold), kept as they
 // lie in memory so that a prefetched chunk costs no more registers than it has
 // bytes.
