@@ -1354,8 +1354,10 @@ hipError_t run_product(LinArgs a, int tile, hipStream_t s) {
     if (grid > 0) {
         if (grid > INT32_MAX) return hipErrorInvalidValue;
         const dim3 gr((unsigned)grid, (unsigned)a.splits);
-        if (tile == 256) k_product<T, KIND, 256><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
-        else k_product<T, KIND, 128><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
+        if constexpr (sizeof(T) == 2) {
+            if (tile == 256) k_product<T, KIND, 256><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
+        }
+        if (tile == 128) k_product<T, KIND, 128><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
     }
     if (a.splits > 1) {
         const int64_t all = KIND == kDw ? (int64_t)a.G * a.rows : a.M;
@@ -1387,31 +1389,37 @@ hipError_t run_few(const LinArgs &a, hipStream_t s) {
 // TFLOP/s where those reach 1100 (bf16, 16384 x 8192 x 4096), if there are
 // enough of them: on 256 CUs, 160 tiles of 256 took 80, 78 and 87 us (forward,
 // dX and dW, 4096 x 2560 x 4096) against 88, 85 and 114 for four times as many
-// of 128; 128 tiles of 256 took 84, 67 and 86 against 70, 75 and 84.
+// of 128; 128 tiles of 256 took 84, 67 and 86 against 70, 75 and 84.  In fp32,
+// whose matrix instructions take 16 times as long, tiles of 128 are never
+// starved: 8192 x 8192 x 2048 1908, 1899 and 1909 us against 1950, 1926 and
+// 2142, 4096 x 5120 x 1024 365, 298 and 471 against 503, 1197 and 1050.
 //
 // A sum is split where the tiles leave CUs without work.  In units of a step's
 // time in bf16 (about 0.4 us with a workgroup a CU): the join's launch costs 8,
 // its partial tiles, written and read, 1/8 each; fp32's steps take four times
 // as long and more, and those of a single row tile, whose other operand comes
 // from memory, twice (32 rows by 16384 x 4096, 128 tiles of 64 steps: 45 us,
-// in two splits 41).  Measured in bf16 with 1, 2, 4 and 8 splits (us): 32 tiles
-// of 64 steps 27, 21, 19, 22; 64 tiles of 64 steps 28, 24, 28, 32; 128 tiles of
-// 64 steps 30, 34 (two), 64 tiles of 256 steps 92, 61, 55, 64; 64 tiles of 32
-// steps 16, 19, 22, 28.
+// in two splits 41).  In fp32, where a CU's workgroups take turns at its matrix
+// units, an uneven last round is evened out too.  Measured in bf16 with 1, 2, 4
+// and 8 splits (us): 32 tiles of 64 steps 27, 21, 19, 22; 64 tiles of 64 steps
+// 28, 24, 28, 32; 128 tiles of 64 steps 30, 34 (two), 64 tiles of 256 steps 92,
+// 61, 55, 64; 64 tiles of 32 steps 16, 19, 22, 28.
 struct Shape {
     int tile, splits;
 };
 Shape pick_shape(int64_t rows, int64_t cols, int64_t groups, int64_t steps, int dtype) {
+    const bool f32 = dtype == FK_F32;
     Shape s;
     const int64_t big = cdiv(rows, 256) * cdiv(cols, 256) * groups;
-    s.tile = rows > 128 && big >= kCus * 5 / 8 ? 256 : 128;
+    s.tile = !f32 && rows > 128 && big >= kCus * 5 / 8 ? 256 : 128;
     s.splits = 1;
     if (s.tile == 256) return s;
     const int64_t tiles = cdiv(rows, 128) * cdiv(cols, 128) * groups;
-    const int64_t unit = dtype == FK_F32 ? 4 : rows <= 128 ? 2 : 1;
-    int64_t best = 8 * steps * unit;  // (in eighths)
-    for (int n = 2; n <= 16 && n <= steps && tiles * n <= kCus; n *= 2) {
-        const int64_t cost = 8 * cdiv(steps, n) * unit + 64 + tiles * n;
+    const int64_t unit = 8 * (f32 ? 4 : rows <= 128 ? 2 : 1);  // (costs in eighths)
+    const int64_t most = f32 ? 4 * kCus : kCus;
+    int64_t best = cdiv(tiles, kCus) * steps * unit;
+    for (int n = 2; n <= 32 && n <= steps && tiles * n <= most; ++n) {
+        const int64_t cost = cdiv(tiles * n, kCus) * cdiv(steps, n) * unit + 64 + tiles * n;
         if (cost < best) best = cost, s.splits = n;
     }
     return s;
