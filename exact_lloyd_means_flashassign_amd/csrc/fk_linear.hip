@@ -590,9 +590,10 @@ struct Epilogue {
 // (1480); with gelu and a residual in the epilogue the
 // forward pass takes 960.  In the loop the matrix units are busy 77 % of the
 // time (the loads' issue costs about 12 %), and a workgroup's first loads and last stores, which nothing overlaps with one
-// workgroup a CU, about 15 us of its 100.  In fp32 tiles of 128 reach 145
-// TFLOP/s (4096 x 1024 x 4096, the library 149) where the tiles divide the CUs
-// evenly, and 63 where they do not (5003 x 1001 x 769: 320 tiles on 256 CUs).
+// workgroup a CU, about 15 us of its 100.  In fp32 tiles of 128 reach 150
+// TFLOP/s (8192 x 8192 x 2048 forward 1876 us, the library 1852), and 60 where
+// a few tiles are left for a second round (5003 x 1001 x 769: 320 tiles on 256
+// CUs, 120 us).
 template <typename T, int KIND, int BS>
 __global__ __launch_bounds__(kTileThreads)
 __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void k_product(LinArgs a, int64_t mtiles,
