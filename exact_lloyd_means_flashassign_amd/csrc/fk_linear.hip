@@ -590,7 +590,7 @@ struct Epilogue {
 // (1480); with gelu and a residual in the epilogue the
 // forward pass takes 960.  In the loop the matrix units are busy 77 % of the
 // time (the loads' issue costs about 12 %), and a workgroup's first loads and last stores, which nothing overlaps with one
-// workgroup a CU, about 15 us of its 100.  In fp32 tiles of 128 reach 150
+// workgroup a CU, about 15 us of its 100.  In fp32 tiles of 128 reach 147
 // TFLOP/s (8192 x 8192 x 2048 forward 1876 us, the library 1852), and 60 where
 // a few tiles are left for a second round (5003 x 1001 x 769: 320 tiles on 256
 // CUs, 120 us).
