@@ -1185,7 +1185,8 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
 // Bound by memory.  Workgroups in turn take neighbouring columns of the same
 // rows, so that whole rows are read together: with neighbouring rows' pieces of
 // 512 bytes instead, 32768 x 4096 in bf16 with a thin dX took 291 against 261
-// us by slots and 248 against 229 without.
+// us by slots and 248 against 229 without (16384 x 4096, half of which the last
+// cache holds, 133 against 137).
 constexpr int kGradRows = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int64_t ldd, int df32, T *dZ, int64_t lddz,
