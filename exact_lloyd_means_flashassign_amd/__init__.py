@@ -196,21 +196,37 @@ def _stream(device):
 _ws_cache = {}
 
 
+def _capturing(d: int) -> bool:
+    """Whether the current stream of device index d is recording a graph."""
+    if torch.cuda.current_device() == d:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(d):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _workspace(nbytes: int, device, workspace=None):
-    """(pointer, size) of a 256-byte aligned device workspace of >= nbytes."""
+    """(pointer, size, owner) of a 256-byte aligned device workspace of >=
+    nbytes; the caller keeps `owner` until its launches are made.  A buffer is
+    kept for every stream and grows with its calls.  A call that a graph
+    records gets one of its own instead, from the graph's memory: the graph
+    holds its address for as long as it is replayed, whatever the stream's own
+    buffer has become by then."""
     if workspace is not None:
         _dev(workspace, "workspace", torch.uint8)
-        return workspace.data_ptr(), workspace.numel()
+        return workspace.data_ptr(), workspace.numel(), workspace
     dev_index = device.index if device.index is not None else torch.cuda.current_device()
-    key = (dev_index, torch.cuda.current_stream(dev_index).cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes + 256:
-        _ws_cache.pop(key, None)
+    if _capturing(dev_index):
         buf = torch.empty(max(nbytes, 1) + 256, dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
+    else:
+        key = (dev_index, torch.cuda.current_stream(dev_index).cuda_stream)
+        buf = _ws_cache.get(key)
+        if buf is None or buf.numel() < nbytes + 256:
+            _ws_cache.pop(key, None)
+            buf = torch.empty(max(nbytes, 1) + 256, dtype=torch.uint8, device=device)
+            _ws_cache[key] = buf
     base = buf.data_ptr()
     pad = (-base) % 256
-    return base + pad, buf.numel() - pad
+    return base + pad, buf.numel() - pad, buf
 
 
 def fk_workspace_size(N: int, d: int, K: int, metric="l2", chunk_rows: int = 0) -> int:
@@ -224,8 +240,8 @@ def _ws_args(N, d, K, metric, device, workspace, chunk_rows=0):
     need = load().fk_workspace_size(int(N), int(d), int(K), _metric(metric), int(chunk_rows))
     if need == 0:
         need = 256  # sizes invalid: the library reports which
-    p, n = _workspace(need, device, workspace)
-    return ctypes.c_void_p(p), ctypes.c_size_t(n)
+    p, n, owner = _workspace(need, device, workspace)
+    return ctypes.c_void_p(p), ctypes.c_size_t(n), owner
 
 
 def fk_assign(X, C, metric="l2", assign=None, min_dist=None, with_min_dist=False, workspace=None, score="fp32"):
@@ -244,7 +260,7 @@ def fk_assign(X, C, metric="l2", assign=None, min_dist=None, with_min_dist=False
         min_dist = torch.empty(N, dtype=torch.float32, device=X.device)
     if min_dist is not None:
         _dev(min_dist, "min_dist", torch.float32, (N,))
-    ws, wsn = _ws_args(N, d, K, metric, X.device, workspace)
+    ws, wsn, _owner = _ws_args(N, d, K, metric, X.device, workspace)
     _check(load().fk_assign(_ptr(X), N, d, _ptr(C), K, _metric(metric), _score(score), _ptr(assign),
                             _ptr(min_dist), ws, wsn, _stream(X.device)))
     return assign, min_dist
@@ -260,7 +276,7 @@ def fk_sort_inverse(assign, K: int, perm=None, offsets=None, workspace=None):
         offsets = torch.empty(K + 1, dtype=torch.int32, device=assign.device)
     _dev(perm, "perm", torch.int32, (N,))
     _dev(offsets, "offsets", torch.int32, (K + 1,))
-    ws, wsn = _ws_args(N, 1, K, "l2", assign.device, workspace)
+    ws, wsn, _owner = _ws_args(N, 1, K, "l2", assign.device, workspace)
     _check(load().fk_sort_inverse(_ptr(assign), N, int(K), _ptr(perm), _ptr(offsets), ws, wsn,
                                   _stream(assign.device)))
     return perm, offsets
@@ -279,7 +295,7 @@ def fk_update(X, assign, C_prev, metric="l2", C_out=None, counts=None, workspace
         counts = torch.empty(K, dtype=torch.int32, device=X.device)
     _dev(C_out, "C_out", torch.float32, (K, d))
     _dev(counts, "counts", torch.int32, (K,))
-    ws, wsn = _ws_args(N, d, K, metric, X.device, workspace)
+    ws, wsn, _owner = _ws_args(N, d, K, metric, X.device, workspace)
     _check(load().fk_update(_ptr(X), N, d, _ptr(assign), K, _metric(metric), _ptr(C_prev), _ptr(C_out),
                             _ptr(counts), ws, wsn, _stream(X.device)))
     return C_out, counts
@@ -307,7 +323,7 @@ def fk_lloyd_iter(X, C_in, metric="l2", assign=None, C_out=None, counts=None, mi
     _dev(counts, "counts", torch.int32, (K,))
     if min_dist is not None:
         _dev(min_dist, "min_dist", torch.float32, (N,))
-    ws, wsn = _ws_args(N, d, K, metric, X.device, workspace)
+    ws, wsn, _owner = _ws_args(N, d, K, metric, X.device, workspace)
     _check(load().fk_lloyd_iter(_ptr(X), N, d, _ptr(C_in), K, _metric(metric), _score(score), _ptr(assign),
                                 _ptr(min_dist), _ptr(C_out), _ptr(counts), ws, wsn, _stream(X.device)))
     return assign, C_out, counts, min_dist
@@ -354,7 +370,7 @@ def fk_lloyd_iter_stream(X_host, C_in, chunk_rows: int, metric="l2", assign_host
         counts = torch.empty(K, dtype=torch.int32, device=C_in.device)
     _dev(C_out, "C_out", torch.float32, (K, d))
     _dev(counts, "counts", torch.int32, (K,))
-    ws, wsn = _ws_args(N, d, K, metric, C_in.device, workspace, chunk_rows=chunk_rows)
+    ws, wsn, _owner = _ws_args(N, d, K, metric, C_in.device, workspace, chunk_rows=chunk_rows)
     _check(load().fk_lloyd_iter_stream(_ptr(X_host), N, d, _ptr(C_in), K, _metric(metric), _score(score),
                                        int(chunk_rows), _ptr(assign_host), _ptr(C_out), _ptr(counts), ws, wsn,
                                        _stream(C_in.device)))
@@ -400,7 +416,7 @@ def fk_fit(X, C_init=None, n_iter: int = 20, metric="l2", K=None, seed: int = 0,
     if C_out.numel() < Ku * d or counts.numel() < Ku:
         raise ValueError("C_out and counts must hold K' rows")
     need = load().fk_fit_workspace_size(int(N), int(d), K, _metric(metric)) or 256
-    p, n = _workspace(need, X.device, workspace)
+    p, n, _owner = _workspace(need, X.device, workspace)
     info = _FitInfo()
     _check(load().fk_fit(_ptr(X), N, d, K, _metric(metric), _score(score), _ptr(C_init), int(seed) & (2 ** 64 - 1),
                          int(n_iter), float(tol), _ptr(C_out), _ptr(assign), _ptr(counts), ctypes.byref(info),
@@ -444,7 +460,7 @@ def fk_ivf_build(X, nlist: int, init_idx=None, n_iter: int = 20, metric="l2", se
            "ids": torch.empty(N, dtype=torch.int32, device=dev),
            "data": torch.empty((N, d), dtype=torch.float32, device=dev)}
     need = load().fk_ivf_workspace_size(int(N), int(d), nlist, _metric(metric)) or 256
-    p, n = _workspace(need, dev, workspace)
+    p, n, _owner = _workspace(need, dev, workspace)
     nl = ctypes.c_int32(0)
     _check(load().fk_ivf_build(_ptr(X), N, d, nlist, _metric(metric), _score(score), int(n_iter),
                                None if idx is None else ctypes.c_void_p(idx.ctypes.data), int(seed) & (2 ** 64 - 1),
@@ -480,7 +496,7 @@ def fk_knn(Q, DB, k: int, metric="l2", idx=None, dist=None, workspace=None, scor
     _dev(idx, "idx", torch.int32, (M, k))
     _dev(dist, "dist", torch.float32, (M, k))
     need = load().fk_knn_workspace_size(int(M), int(d), int(Ndb), k, _metric(metric)) or 256
-    p, n = _workspace(need, Q.device, workspace)
+    p, n, _owner = _workspace(need, Q.device, workspace)
     _check(load().fk_knn(_ptr(Q), M, d, _ptr(DB), Ndb, k, _metric(metric), _score(score), _ptr(idx), _ptr(dist),
                          ctypes.c_void_p(p), ctypes.c_size_t(n), _stream(Q.device)))
     return idx, dist
@@ -554,12 +570,12 @@ def _run(fn, d, *args):
 
 def _scratch(nbytes, d, workspace):
     """_workspace for device index d."""
-    if workspace is None:
+    if workspace is None and not _capturing(d):
         buf = _ws_cache.get((d, _raw_stream(d)))
         if buf is not None and buf.numel() >= nbytes + 256:
             base = buf.data_ptr()
             pad = -base % 256
-            return base + pad, buf.numel() - pad
+            return base + pad, buf.numel() - pad, buf
     return _workspace(nbytes, torch.device("cuda", d), workspace)
 
 
@@ -617,7 +633,7 @@ def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = Tru
         db = torch.empty_like(weight) if with_bias else None
     dev = _one_device(dY, X, mean, rstd, weight, dX)
     need = load().fk_layer_norm_backward_workspace_size(rows, d) or 256
-    p, n = _scratch(need, dev, workspace)
+    p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_layer_norm_backward, dev, DTYPES[X.dtype], DTYPES[X.dtype if weight is None else weight.dtype],
          _at(dY), ldd, _at(X), ldx, rows, d, _at(mean), _at(rstd), _at(weight), _at(dX), lddx, _at(dw), _at(db), p, n)
     return dX, dw, db
@@ -649,7 +665,7 @@ def fk_route(logits, k: int, norm="chosen", valid=None, workspace=None):
     losses = torch.empty(2, dtype=torch.float32, device=logits.device)
     live = torch.empty(1, dtype=torch.int32, device=logits.device)
     need = load().fk_route_workspace_size(T, E) or 256
-    p, n = _scratch(need, dev, workspace)
+    p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_route, dev, DTYPES[logits.dtype], _at(logits), ldl, T, E, k, _named(GATES, norm, "gate norm"),
          _at(valid), _at(ids), _at(gates), _at(counts), _at(losses), _at(live), p, n)
     return ids, gates, counts, losses, live
@@ -739,7 +755,7 @@ def fk_linear(X, W, bias=None, act="none", residual=None, slots=None, offsets=No
     pre = torch.empty(shape, dtype=X.dtype, device=X.device) if with_pre else None
     dev = _one_device(X, W, bias, residual, slots, offsets, Y)
     need = load().fk_linear_workspace_size(ctypes.byref(h), 0) or 256
-    p, n = _scratch(need, dev, workspace)
+    p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_linear, dev, ctypes.byref(h), _at(X), _at(W), _at(bias), _at(residual), _at(slots), _at(offsets),
          _at(Y), _at(pre), p, n)
     return Y, pre
@@ -769,7 +785,7 @@ def fk_linear_backward(dY, X, W, act="none", pre=None, slots=None, offsets=None,
     dW = torch.empty(W.shape, dtype=X.dtype, device=X.device) if with_dw else None
     db = torch.empty(W.shape[:-1], dtype=bias_dtype, device=X.device) if with_bias else None
     need = load().fk_linear_workspace_size(ctypes.byref(h), 1) or 256
-    p, n = _scratch(need, dev, workspace)
+    p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_linear_backward, dev, ctypes.byref(h), _at(dY), _at(X), _at(W), _at(pre), _at(slots), _at(offsets),
          _at(dX), _at(dW), _at(db), p, n)
     return dX, dW, db
