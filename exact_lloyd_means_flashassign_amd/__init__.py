@@ -7,15 +7,17 @@ of the computation runs in the HIP kernels of ``libfk.so``; torch is used only
 for device memory and streams.  If ``libfk.so`` has not been built, ``load()``
 raises -- there is no fallback path.
 
-The workspace is cached per (device, stream) and reused by every call on that
-stream that does not pass its own ``workspace`` (calls on one stream run in
-order, so they may share it).
+Each thread caches a workspace per (device, stream) and reuses it in every call
+on that stream that does not pass its own ``workspace`` (a thread's calls on
+one stream run in order, so they may share it); a call that a graph records has
+one of its own.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import re
+import threading
 
 import torch
 
@@ -193,7 +195,23 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-_ws_cache = {}
+class _Buffers(threading.local):
+    """A thread's scratch buffers by (device index, stream).  The calls release
+    the interpreter's lock while they enqueue their kernels, so two threads that
+    use one stream (the caller's and the autograd engine's, for one) may enqueue
+    theirs in turns: each has buffers of its own, which go when it ends."""
+
+    def __init__(self):
+        self.by_stream = {}
+
+    def __len__(self):
+        return len(self.by_stream)
+
+    def clear(self):
+        self.by_stream.clear()
+
+
+_ws_cache = _Buffers()
 
 
 def _capturing(d: int) -> bool:
@@ -207,10 +225,10 @@ def _capturing(d: int) -> bool:
 def _workspace(nbytes: int, device, workspace=None):
     """(pointer, size, owner) of a 256-byte aligned device workspace of >=
     nbytes; the caller keeps `owner` until its launches are made.  A buffer is
-    kept for every stream and grows with its calls.  A call that a graph
-    records gets one of its own instead, from the graph's memory: the graph
-    holds its address for as long as it is replayed, whatever the stream's own
-    buffer has become by then."""
+    kept for every stream of a thread and grows with its calls.  A call that a
+    graph records gets one of its own instead, from the graph's memory: the
+    graph holds its address for as long as it is replayed, whatever the
+    stream's own buffer has become by then."""
     if workspace is not None:
         _dev(workspace, "workspace", torch.uint8)
         return workspace.data_ptr(), workspace.numel(), workspace
@@ -219,11 +237,11 @@ def _workspace(nbytes: int, device, workspace=None):
         buf = torch.empty(max(nbytes, 1) + 256, dtype=torch.uint8, device=device)
     else:
         key = (dev_index, torch.cuda.current_stream(dev_index).cuda_stream)
-        buf = _ws_cache.get(key)
+        buf = _ws_cache.by_stream.get(key)
         if buf is None or buf.numel() < nbytes + 256:
-            _ws_cache.pop(key, None)
+            _ws_cache.by_stream.pop(key, None)
             buf = torch.empty(max(nbytes, 1) + 256, dtype=torch.uint8, device=device)
-            _ws_cache[key] = buf
+            _ws_cache.by_stream[key] = buf
     base = buf.data_ptr()
     pad = (-base) % 256
     return base + pad, buf.numel() - pad, buf
@@ -571,7 +589,7 @@ def _run(fn, d, *args):
 def _scratch(nbytes, d, workspace):
     """_workspace for device index d."""
     if workspace is None and not _capturing(d):
-        buf = _ws_cache.get((d, _raw_stream(d)))
+        buf = _ws_cache.by_stream.get((d, _raw_stream(d)))
         if buf is not None and buf.numel() >= nbytes + 256:
             base = buf.data_ptr()
             pad = -base % 256

@@ -1,5 +1,6 @@
 """The binding's workspaces, with host memory in the place of the device's:
 which buffer a call gets, and which ones stay."""
+import threading
 import types
 
 import pytest
@@ -70,3 +71,16 @@ def test_a_given_workspace_is_taken_as_it_is(card, monkeypatch):
         assert fk._workspace(100, DEV, mine)[:2] == (mine.data_ptr(), 4096)
         assert fk._scratch(100, 0, mine)[:2] == (mine.data_ptr(), 4096)
     assert not fk._ws_cache
+
+
+@pytest.mark.parametrize("i", (0, 1))
+def test_threads_of_one_stream_have_buffers_of_their_own(card, i):
+    """A call's kernels may be enqueued between those of another thread's call."""
+    get = calls()[i]
+    mine = get(5000)
+    theirs = []
+    t = threading.Thread(target=lambda: theirs.extend((get(5000), get(300))))
+    t.start()
+    t.join()
+    assert theirs[0][0] == theirs[1][0] != mine[0]
+    assert get(300)[:2] == mine[:2]
