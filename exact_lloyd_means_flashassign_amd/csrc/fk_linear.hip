@@ -80,16 +80,34 @@ struct Mma<float> {
 };
 
 // ---- activations ----------------------------------------------------------------
+//
+// In two forms, each to the accuracy of what it is for.  FINE, for results that
+// leave in fp32: the mathematical library's exponential and complementary error
+// function and a correctly rounded quotient, a few ulp of the result, small
+// results too.  Otherwise, for results that are rounded to 16 bits: the
+// hardware's exponential and reciprocal and an approximation of erf, good to
+// 1.5e-7 of |z| where the rounding alone takes 4.9e-4 (fp16) or more of the
+// result, at about a third of the instructions.
 
 // 2^x and 1/x by the hardware's instructions (about an ulp each); an infinite
 // 2^x gives a logistic of 0.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
-__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
+template <bool FINE>
+__device__ __forceinline__ float logistic(float x) {
+    if constexpr (FINE) return 1.0f / (1.0f + expf(-x));
+    else return __builtin_amdgcn_rcpf(1.0f + exp_of(-x));
+}
 
-// (1 + erf(z / sqrt 2)) / 2 by the rational approximation 7.1.26 of Abramowitz
-// and Stegun, Handbook of Mathematical Functions (1964), whose error is below
-// 1.5e-7 in erf, and e^(-z^2/2), which it needs anyway.
+// (1 + erf(z / sqrt 2)) / 2, and e^(-z^2/2).  The fast form by the rational
+// approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions (1964), whose error is below 1.5e-7 in erf and which needs the
+// exponential anyway.
+template <bool FINE>
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
+    if constexpr (FINE) {
+        e = expf(-0.5f * z * z);
+        return 0.5f * erfcf(-0.707106781f * z);
+    }
     const float x = fabsf(z) * 0.707106781f;
     const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
     float p = 1.061405429f;
@@ -106,7 +124,7 @@ __device__ __forceinline__ float normal_cdf(float z, float &e) {
 __device__ __forceinline__ float tanh_arg(float z) { return 1.59576912f * (z + 0.044715f * z * z * z); }
 
 // the activation of N values (the choice outside their loop)
-template <int N>
+template <bool FINE, int N>
 __device__ __forceinline__ void activate(int act, float (&z)[N]) {
     if (act == FK_ACT_RELU) {
 #pragma unroll
@@ -115,20 +133,20 @@ __device__ __forceinline__ void activate(int act, float (&z)[N]) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float e;
-            z[i] *= normal_cdf(z[i], e);
+            z[i] *= normal_cdf<FINE>(z[i], e);
         }
     } else if (act == FK_ACT_GELU_TANH) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] *= logistic(tanh_arg(z[i]));
+        for (int i = 0; i < N; ++i) z[i] *= logistic<FINE>(tanh_arg(z[i]));
     } else if (act == FK_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] *= logistic(z[i]);
+        for (int i = 0; i < N; ++i) z[i] *= logistic<FINE>(z[i]);
     }
 }
 
 // d[i] *= the activation's slope at z[i].  Where the slope has come to its
 // limit (0 or 1), z is held back so that its powers stay finite.
-template <int N>
+template <bool FINE, int N>
 __device__ __forceinline__ void times_slope(int act, const float (&z)[N], float (&d)[N]) {
     if (act == FK_ACT_RELU) {
 #pragma unroll
@@ -138,21 +156,21 @@ __device__ __forceinline__ void times_slope(int act, const float (&z)[N], float 
         for (int i = 0; i < N; ++i) {
             const float c = z[i] != z[i] ? z[i] : fminf(fmaxf(z[i], -64.0f), 64.0f);
             float e;
-            const float s = normal_cdf(c, e);
+            const float s = normal_cdf<FINE>(c, e);
             d[i] *= s + c * e * 0.398942280f;
         }
     } else if (act == FK_ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float c = z[i] != z[i] ? z[i] : fminf(fmaxf(z[i], -64.0f), 64.0f);
-            const float s = logistic(tanh_arg(c));
+            const float s = logistic<FINE>(tanh_arg(c));
             d[i] *= s + c * s * (1.0f - s) * 1.59576912f * (1.0f + 0.134145f * c * c);
         }
     } else if (act == FK_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float c = z[i] != z[i] ? z[i] : fminf(fmaxf(z[i], -128.0f), 128.0f);
-            const float s = logistic(c);
+            const float s = logistic<FINE>(c);
             d[i] *= s * (1.0f + c * (1.0f - s));
         }
     }
@@ -523,10 +541,28 @@ struct Epilogue {
             for (int i = 0; i < 8; ++i) v[i] = (float)c[i / E].e[i % E];
         }
     };
-    template <bool SURE, int N>
+    // GRAD: a gradient's product, which has no bias, activation or residual.
+    template <bool SURE, bool GRAD, int N>
     __device__ __forceinline__ void out(const LinArgs &a, int g, const int64_t (&crow)[N], float (&v)[N * 8],
                                         const Eight *res) const {
         if (!SURE && n == 0) return;
+        if constexpr (!GRAD) finish<SURE>(a, crow, v, res);
+        const int64_t first = (int64_t)g * a.gsc + col;
+        if (sizeof(T) != 4 && a.cf32) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (SURE || crow[k] >= 0)
+                    Epilogue<float>::template put<SURE>((float *)a.C + first + crow[k] * a.ldc, *(const float(*)[8])(v + k * 8), n);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (SURE || crow[k] >= 0)
+                    put<SURE>((T *)a.C + first + crow[k] * a.ldc, *(const float(*)[8])(v + k * 8), n);
+        }
+    }
+    template <bool SURE, int N>
+    __device__ __forceinline__ void finish(const LinArgs &a, const int64_t (&crow)[N], float (&v)[N * 8],
+                                           const Eight *res) const {
         float r[N][8];
         if (a.R != nullptr) {
 #pragma unroll
@@ -548,24 +584,13 @@ struct Epilogue {
                 if (SURE || crow[k] >= 0)
                     put<SURE>((T *)a.Z + crow[k] * a.ldz + col, *(const float(*)[8])(v + k * 8), n);
         }
-        activate(a.act, v);
+        if (sizeof(T) == 4 || a.cf32) activate<true>(a.act, v);
+        else activate<false>(a.act, v);
         if (a.R != nullptr) {
 #pragma unroll
             for (int k = 0; k < N; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k * 8 + i] += r[k][i];
-        }
-        const int64_t first = (int64_t)g * a.gsc + col;
-        if (sizeof(T) != 4 && a.cf32) {
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (SURE || crow[k] >= 0)
-                    Epilogue<float>::template put<SURE>((float *)a.C + first + crow[k] * a.ldc, *(const float(*)[8])(v + k * 8), n);
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (SURE || crow[k] >= 0)
-                    put<SURE>((T *)a.C + first + crow[k] * a.ldc, *(const float(*)[8])(v + k * 8), n);
         }
     }
 };
@@ -915,7 +940,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     // the first half of a row's lanes: the wave's columns in B's first part
     const int lc = lane % LPR;
     const int64_t col = c0 + lc / (LPR / 2) * (BN / 2) + wn + lc % (LPR / 2) * 8;
-    if ((SPLITS && a.splits > 1) || rest) {
+    if (KIND != kFwd || (SPLITS && a.splits > 1) || rest) {
         ep.col = col;
         const int64_t left = a.N - col;
         ep.n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
@@ -946,7 +971,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     };
     // the residual of a batch, sent for a batch ahead
     typename Epilogue<T>::Eight res[BATCH];
-    const bool added = sure && a.R != nullptr;
+    const bool added = KIND == kFwd && sure && a.R != nullptr;
     auto send_for = [&](int p, int q) {
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
@@ -1014,7 +1039,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                     if (q + BATCH * RPP < ROWS) send_for(p, q + BATCH * RPP);
                     else if (p == 0) send_for(1, 0);
                 }
-                ep.template out<true>(a, t.g, crow, v, now);
+                ep.template out<true, KIND != kFwd>(a, t.g, crow, v, now);
                 continue;
             }
 #pragma unroll
@@ -1024,7 +1049,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
                 for (int k = 0; k < BATCH; ++k)
                     if (crow[k] >= 0) ep.zero(a, crow[k]);
             } else {
-                ep.template out<false>(a, t.g, crow, v, nullptr);
+                ep.template out<false, KIND != kFwd>(a, t.g, crow, v, nullptr);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -1082,7 +1107,7 @@ __global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
         for (int i = 0; i < 8; ++i) v[i] += w[i];
     }
     const int64_t rows[1] = {crow};
-    ep.template out<false>(a, g, rows, v, nullptr);
+    ep.template out<false, false>(a, g, rows, v, nullptr);
 }
 
 // ---- a few rows against a whole weight matrix -----------------------------------------
@@ -1171,7 +1196,7 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
         Epilogue<T> ep;
         ep.init(a, g, n0 + c);
         const int64_t rows[1] = {a.cmap(p0 + m)};
-        ep.template out<false>(a, g, rows, v, nullptr);
+        ep.template out<false, false>(a, g, rows, v, nullptr);
     }
 }
 
@@ -1221,7 +1246,7 @@ __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int
             else Epilogue<T>::template get<SURE>((const T *)dY + row * ldd + col, d, n);
             if (a.act != FK_ACT_NONE) {
                 Epilogue<T>::template get<SURE>((const T *)a.Z + row * a.ldz + col, z, n);
-                times_slope(a.act, z, d);
+                times_slope<sizeof(T) == 4>(a.act, z, d);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
