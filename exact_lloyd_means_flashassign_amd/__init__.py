@@ -214,8 +214,11 @@ class _Buffers(threading.local):
 _ws_cache = _Buffers()
 
 
-def _capturing(d: int) -> bool:
-    """Whether the current stream of device index d is recording a graph."""
+def _capturing(d: int, stream: int) -> bool:
+    """Whether `stream`, the current one of device index d, is recording a graph
+    (the default stream, 0, cannot)."""
+    if stream == 0:
+        return False
     if torch.cuda.current_device() == d:
         return torch.cuda.is_current_stream_capturing()
     with torch.cuda.device(d):
@@ -233,10 +236,11 @@ def _workspace(nbytes: int, device, workspace=None):
         _dev(workspace, "workspace", torch.uint8)
         return workspace.data_ptr(), workspace.numel(), workspace
     dev_index = device.index if device.index is not None else torch.cuda.current_device()
-    if _capturing(dev_index):
+    stream = torch.cuda.current_stream(dev_index).cuda_stream
+    if _capturing(dev_index, stream):
         buf = torch.empty(max(nbytes, 1) + 256, dtype=torch.uint8, device=device)
     else:
-        key = (dev_index, torch.cuda.current_stream(dev_index).cuda_stream)
+        key = (dev_index, stream)
         buf = _ws_cache.by_stream.get(key)
         if buf is None or buf.numel() < nbytes + 256:
             _ws_cache.by_stream.pop(key, None)
@@ -588,8 +592,9 @@ def _run(fn, d, *args):
 
 def _scratch(nbytes, d, workspace):
     """_workspace for device index d."""
-    if workspace is None and not _capturing(d):
-        buf = _ws_cache.by_stream.get((d, _raw_stream(d)))
+    if workspace is None:
+        stream = _raw_stream(d)
+        buf = None if _capturing(d, stream) else _ws_cache.by_stream.get((d, stream))
         if buf is not None and buf.numel() >= nbytes + 256:
             base = buf.data_ptr()
             pad = -base % 256
