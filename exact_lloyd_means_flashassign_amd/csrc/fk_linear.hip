@@ -738,7 +738,11 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     // All but the latest `later` loads to LDS have arrived, in every wave
     // (vmcnt, which counts a wave's loads in order; the other counters are left
     // alone), and every wave has read what it read (the compiler's wait before
-    // the barrier).
+    // the barrier).  The compiler does not know what the loads in assembly write,
+    // so what keeps them apart from the reads of the same place is that one of
+    // these barriers, which no access to LDS crosses, lies between them both ways.
+    // Nothing but loads to LDS is under way in the loop: another load among them
+    // can only make the wait longer.
     auto landed = [&](auto later) {
         constexpr int n = decltype(later)::value;
         __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
@@ -978,13 +982,12 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
             res[k].load((const T *)a.R + row_at(p, q, k) * a.ldr + col);
         }
     };
-    // the tiles are read to the end, and no load to LDS is under way
-    if (added) {
-        send_for(0, 0);
-        landed(std::integral_constant<int, BATCH * (int)sizeof(T) / 2>{});
-    } else {
-        landed(c0_);
-    }
+    // the tiles are read to the end, and no load to LDS is under way; only then
+    // the first batch's residual is sent for, whose loads are the compiler's and
+    // so not to be counted on in a wait (they are back by the time the first
+    // part is staged)
+    landed(c0_);
+    if (added) send_for(0, 0);
 #pragma unroll 1
     for (int p = 0; p < 2; ++p) {
         // (the empty statements keep the compiler from making one block of the
