@@ -937,7 +937,8 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
     constexpr int LPR = CH / 2;          // lanes that write a row of C
     constexpr int RPP = 64 / LPR;        // rows that a wave writes at once
     constexpr int ROWS = TB * 32;        // rows of a part
-    constexpr int BATCH = 4;  // rows a lane takes at a time
+    // rows a lane takes at a time (with four, tiles of 128 spill)
+    constexpr int BATCH = BS == 128 ? 2 : 4;
     static_assert(4 * ROWS * CH * 16 <= sizeof(smem), "the staged rows fit the tiles");
     v4f *stage = reinterpret_cast<v4f *>(smem) + wave * ROWS * CH;
     Epilogue<T> ep;
