@@ -37,13 +37,27 @@ fk_status check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, si
     return FK_OK;
 }
 
+// What an argument takes up: `bytes` from p on, of a matrix only `width` out of
+// every `pitch`.
 struct Span {
     const void *p;
     size_t bytes;
     const char *name;
+    size_t width = 0, pitch = 0;
 };
 Span matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, size_t size, const char *name) {
-    return {p, rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * size : 0, name};
+    return {p, rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * size : 0, name, (size_t)cols * size,
+            (size_t)ld * size};
+}
+
+// Whether two spans have a byte in common.  Matrices of one pitch may lie in
+// each other's gaps: column slices of one buffer.
+bool share_bytes(const Span &a, const Span &b) {
+    if (!overlap(a.p, a.bytes, b.p, b.bytes)) return false;
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    const size_t far = pb >= pa ? (pb - pa) % a.pitch : a.pitch - 1 - (pa - pb - 1) % a.pitch;  // b's rows after a's
+    return far < a.width || far + b.width > a.pitch;
 }
 
 // No output overlaps an input or another output.
@@ -53,7 +67,7 @@ fk_status check_apart(const Span *outs, int nout, const Span *ins, int nin) {
         for (int j = 0; j < nin + i; ++j) {
             const Span &o = j < nin ? ins[j] : outs[j - nin];
             if (o.p == nullptr || o.bytes == 0) continue;
-            if (overlap(outs[i].p, outs[i].bytes, o.p, o.bytes))
+            if (share_bytes(outs[i], o))
                 return fail(FK_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, o.name);
         }
     }

@@ -332,7 +332,8 @@ fk_status fk_knn(const float *Q, int64_t M, int32_t d, const float *DB, int64_t 
  * may be further apart than they are long (the ld arguments, in elements), and
  * columns are contiguous.  Every sum, softmax, norm and statistic is fp32 and
  * rounded once to the output's type.  Results are bitwise reproducible (no
- * floating-point atomics).  Outputs must not overlap inputs, except where said.
+ * floating-point atomics).  Outputs must not overlap inputs, except where said
+ * (column slices of one buffer do not overlap).
  * Sizes of zero rows are accepted; gradients of parameters are then zero.
  * NaN and infinities go through by the formulas unless said otherwise.
  */

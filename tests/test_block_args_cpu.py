@@ -1,0 +1,53 @@
+"""Arguments that the expert-block entry points take and refuse, on the CPU: a
+call that passes the checks of its matrices ends at its missing workspace, which
+is asked for after them and before any device call."""
+import ctypes
+
+import pytest
+
+import exact_lloyd_means_flashassign_amd as fk
+from test_block_cpu import BF16, F32, INVALID, WORKSPACE, P, lib, said, shape  # noqa: F401
+
+
+def linear(lib, h, X=0x10000, W=0x2000000, Y=0x3000000, R=0, pre=0):  # noqa: F811
+    return lib.fk_linear(ctypes.byref(h), P(X), P(W), None, P(R), None, None, P(Y), P(pre), None, 0, None)
+
+
+def backward(lib, h, dY=0x10000, X=0x1000000, W=0x2000000, pre=0, dX=0x4000000, dW=0x5000000):  # noqa: F811
+    return lib.fk_linear_backward(ctypes.byref(h), P(dY), P(X), P(W), P(pre), None, None, P(dX), P(dW), None, None, 0,
+                                  None)
+
+
+def norm_backward(lib, dY, X, dX, rows=4, d=64, ld=192):  # noqa: F811
+    return lib.fk_layer_norm_backward(BF16, F32, P(dY), ld, P(X), ld, rows, d, P(0x300000), P(0x400000), None, P(dX), ld,
+                                      None, None, None, 0, None)
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (2, 1, 0), (1, 2, 0)])
+def test_column_slices_of_one_buffer_are_apart(lib, order):  # noqa: F811
+    """Three slices of 64 columns of a buffer with rows of 192 (bf16)."""
+    dY, X, dX = (0x10000 + 128 * i for i in order)
+    assert norm_backward(lib, dY, X, dX) == WORKSPACE
+    # a row further up or down they are as far apart
+    assert norm_backward(lib, dY, X, dX + 384) == WORKSPACE
+    assert norm_backward(lib, dY + 384, X + 384, dX) == WORKSPACE
+    h = shape(M=50, N=32, K=64, ldx=128, ldw=64, ldy=128, ldpre=128, ldr=128)
+    a, b, c = (0x10000 + 64 * i for i in (0, 2, 3))
+    assert linear(lib, h, X=a, Y=b, pre=c) == WORKSPACE
+    assert linear(lib, h, X=a, Y=c, R=b) == WORKSPACE
+
+
+def test_slices_that_meet_are_refused(lib):  # noqa: F811
+    base = 0x10000
+    for off in (2, 126, 384 - 126, 384 - 2):  # into the next slice, or round into the next row
+        assert norm_backward(lib, 0x200000, base, base + off) == INVALID and said(lib, "dX overlaps X"), off
+        assert norm_backward(lib, 0x200000, base + off, base) == INVALID and said(lib, "dX overlaps X"), off
+    assert norm_backward(lib, 0x200000, base, base + 128) == WORKSPACE
+    assert norm_backward(lib, 0x200000, base, base + 256) == WORKSPACE
+    # other row strides may meet anywhere
+    h = shape(M=50, N=32, K=64, ldx=128, ldw=64, ldy=136)
+    assert linear(lib, h, X=0x10000, Y=0x10080) == INVALID and said(lib, "Y overlaps X")
+    # a vector among the rows
+    st = lib.fk_layer_norm_backward(BF16, F32, P(0x200000), 192, P(0x10000), 192, 4, 64, P(0x300000), P(0x400000), None,
+                                    P(0x500000), 192, P(0x10080), None, None, 0, None)
+    assert st == INVALID and said(lib, "dweight overlaps X")
