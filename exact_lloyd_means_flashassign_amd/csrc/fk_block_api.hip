@@ -263,8 +263,12 @@ fk_status check_slots(const fk_linear_shape *h, const int32_t *slots, const int3
     return FK_OK;
 }
 
-fk_status check_16(const void *p, const char *name) {
-    if (!aligned(p, 16)) return fail(FK_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+// Rows of whole 16-byte chunks are read chunk by chunk; others element by
+// element, wherever they start.
+fk_status check_start(const void *p, int64_t cols, int64_t ld, size_t size, const char *name) {
+    const int64_t chunk = 16 / (int64_t)size;
+    if (cols % chunk == 0 && ld % chunk == 0 && !aligned(p, 16))
+        return fail(FK_ERR_INVALID_ARG, "%s must be 16-byte aligned, its rows being whole 16-byte chunks", name);
     return FK_OK;
 }
 
@@ -290,8 +294,8 @@ fk_status fk_linear(const fk_linear_shape *shape, const void *X, const void *W, 
     FK_CHECK(check_matrix(Y, h.M, h.N, h.ldy, ysz, "Y"));
     if (residual) FK_CHECK(check_matrix(residual, h.M, h.N, h.ldr, sz, "residual"));
     if (pre) FK_CHECK(check_matrix(pre, h.M, h.N, h.ldz, sz, "pre"));
-    FK_CHECK(check_16(X, "X"));
-    FK_CHECK(check_16(W, "W"));
+    FK_CHECK(check_start(X, h.K, h.ldx, sz, "X"));
+    FK_CHECK(check_start(W, h.K, h.ldw, sz, "W"));
     if (!aligned(bias, bsz)) return fail(FK_ERR_INVALID_ARG, "bias must be aligned to its elements");
     FK_CHECK(check_slots(shape, slots, offsets));
     const bool in_place = residual == Y && h.ldr == h.ldy && h.dtype == h.ydtype;
@@ -323,9 +327,9 @@ fk_status fk_linear_backward(const fk_linear_shape *shape, const void *dY, const
     if (dW) FK_CHECK(check_matrix(X, xr, h.K, h.ldx, sz, "X"));
     if (dX) FK_CHECK(check_matrix(W, wr, h.K, h.ldw, sz, "W"));
     if (h.act != FK_ACT_NONE) FK_CHECK(check_matrix(pre, h.M, h.N, h.ldz, sz, "pre"));
-    FK_CHECK(check_16(dY, "dY"));
-    FK_CHECK(check_16(X, "X"));
-    FK_CHECK(check_16(W, "W"));
+    FK_CHECK(check_start(dY, h.N, h.ldy, ysz, "dY"));
+    FK_CHECK(check_start(X, h.K, h.ldx, sz, "X"));
+    FK_CHECK(check_start(W, h.K, h.ldw, sz, "W"));
     if (!aligned(dX, sz) || !aligned(dW, sz) || !aligned(dbias, bsz))
         return fail(FK_ERR_INVALID_ARG, "dX, dW and dbias must be aligned to their elements");
     FK_CHECK(check_slots(shape, slots, offsets));

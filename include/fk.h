@@ -421,9 +421,9 @@ fk_status fk_route_backward(int32_t dtype, const void *logits, int64_t ldl, int6
  * pre (may be NULL) receives the pre-activations X W^T + bias, of X's type, for
  * fk_linear_backward.  bias and residual may be NULL; residual may be Y itself
  * (same row stride and type).  X, W, residual and pre are of type dtype, bias
- * of bias_dtype (dtype or FK_F32), Y of ydtype (dtype or FK_F32).  X, W, dY
- * and pre start on 16 bytes; rows of whole 16-byte chunks (K and the row
- * strides multiples of 8, or of 4 in fp32) are read as they lie, others are
+ * of bias_dtype (dtype or FK_F32), Y of ydtype (dtype or FK_F32).  X, W and dY
+ * whose rows are whole 16-byte chunks (columns and row stride multiples of 8, or
+ * of 4 in fp32) are read as they lie and must start on 16 bytes; others are
  * laid out once more in the workspace.  Workspace:
  * fk_linear_workspace_size(shape, 0).
  */

@@ -51,3 +51,21 @@ def test_slices_that_meet_are_refused(lib):  # noqa: F811
     st = lib.fk_layer_norm_backward(BF16, F32, P(0x200000), 192, P(0x10000), 192, 4, 64, P(0x300000), P(0x400000), None,
                                     P(0x500000), 192, P(0x10080), None, None, 0, None)
     assert st == INVALID and said(lib, "dweight overlaps X")
+
+
+def test_where_rows_may_start(lib):  # noqa: F811
+    """Rows of whole 16-byte chunks on 16 bytes; others on their elements."""
+    whole, odd = shape(M=50), shape(M=50, K=127, ldx=127, ldw=127, N=31, ldy=31, ldr=31, ldpre=31)
+    assert linear(lib, whole, X=0x10002) == INVALID and said(lib, "16-byte")
+    assert linear(lib, whole, W=0x2000008) == INVALID and said(lib, "16-byte")
+    assert backward(lib, whole, dY=0x10002) == INVALID and said(lib, "16-byte")
+    for off in (0, 2, 14):
+        assert linear(lib, odd, X=0x10000 + off) == WORKSPACE
+        assert linear(lib, odd, W=0x2000000 + off) == WORKSPACE
+        assert linear(lib, odd, Y=0x3000000 + off, R=0x8000002, pre=0x9000002) == WORKSPACE
+        assert backward(lib, odd, dY=0x10000 + off, X=0x1000000 + off, W=0x2000000 + off) == WORKSPACE
+    assert linear(lib, odd, X=0x10001) == INVALID and said(lib, "elements")
+    # a stride of whole chunks does not make the columns whole
+    assert linear(lib, shape(M=50, K=127), X=0x10002) == WORKSPACE
+    assert linear(lib, shape(M=50, ldx=129), X=0x10002) == WORKSPACE
+    assert backward(lib, shape(act=4), pre=0x9000002) == WORKSPACE  # pre may start anywhere

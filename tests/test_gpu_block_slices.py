@@ -28,3 +28,35 @@ def test_outputs_beside_inputs(gpu_lib, d, dtype):
     Y = rand(140, d, seed=3, dtype=dtype)
     assert torch.equal(fk.fk_combine(Y, 2, residual=a, out=b), fk.fk_combine(Y, 2, residual=x))
     assert torch.equal(a, x) and torch.equal(c, other)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(5, 33, 67), (90, 131, 257)])
+def test_rows_cut_from_odd_matrices(gpu_lib, M, N, K, dtype):
+    """X[1:], W[1:], dY[1:] and pre[1:] with odd widths: none starts on 16 bytes."""
+    fk = gpu_lib
+    log(f"cut rows {M} x {N} x {K} {dtype}")
+    X, Wt = rand(M + 1, K, seed=1, dtype=dtype)[1:], rand(N + 1, K, seed=2, scale=K ** -0.5, dtype=dtype)[1:]
+    b, res = rand(N, seed=3, dtype=dtype), rand(M + 1, N, seed=4, dtype=dtype)[1:]
+    dY, pre = rand(M + 1, N, seed=5, dtype=dtype)[1:], rand(M + 1, N, seed=6, dtype=dtype)[1:]
+    assert all(t.data_ptr() % 16 for t in (X, Wt, res, dY, pre))
+    y, _, e_y, _ = R.linear(X, Wt, b, "silu", res)
+    check("Y", fk.fk_linear(X, Wt, b, act="silu", residual=res)[0], y, e_y, dtype)
+    for name in ("silu", "none"):
+        kept = pre if name == "silu" else None
+        dx, dw, db, e_dx, e_dw, e_db = R.linear_grad(dY, X, Wt, name, kept)
+        dX, dW, dB = fk.fk_linear_backward(dY, X, Wt, act=name, pre=kept)
+        check("dX", dX, dx, e_dx, dtype)
+        check("dW", dW, dw, e_dw, dtype)
+        check("dbias", dB, db, e_db, dtype)
+
+
+def test_pre_off_16_bytes(gpu_lib):
+    """Whole chunks in pre's rows that start on no chunk."""
+    fk = gpu_lib
+    M, N, K = 130, 512, 64
+    X, Wt, dY = rand(M, K, seed=1), rand(N, K, seed=2, scale=0.1), rand(M, N, seed=3)
+    pre = rand(M * N + 1, seed=4)[1:].view(M, N)
+    for got, want in zip(fk.fk_linear_backward(dY, X, Wt, act="gelu", pre=pre),
+                         fk.fk_linear_backward(dY, X, Wt, act="gelu", pre=pre.clone())):
+        assert torch.equal(got, want)
