@@ -777,7 +777,7 @@ def fk_linear(X, W, bias=None, act="none", residual=None, slots=None, offsets=No
         h.ldr = _rows(residual, "residual", (X.dtype,), shape)
     pre = torch.empty(shape, dtype=X.dtype, device=X.device) if with_pre else None
     dev = _one_device(X, W, bias, residual, slots, offsets, Y)
-    need = load().fk_linear_workspace_size(ctypes.byref(h), 0) or 256
+    need = load().fk_linear_workspace_size(ctypes.byref(h), 2 if slots is None else 0) or 256
     p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_linear, dev, ctypes.byref(h), _at(X), _at(W), _at(bias), _at(residual), _at(slots), _at(offsets),
          _at(Y), _at(pre), p, n)
@@ -807,7 +807,7 @@ def fk_linear_backward(dY, X, W, act="none", pre=None, slots=None, offsets=None,
     dX = torch.empty((h.M, h.K), dtype=X.dtype, device=X.device) if with_dx else None
     dW = torch.empty(W.shape, dtype=X.dtype, device=X.device) if with_dw else None
     db = torch.empty(W.shape[:-1], dtype=bias_dtype, device=X.device) if with_bias else None
-    need = load().fk_linear_workspace_size(ctypes.byref(h), 1) or 256
+    need = load().fk_linear_workspace_size(ctypes.byref(h), 3 if slots is None else 1) or 256
     p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_linear_backward, dev, ctypes.byref(h), _at(dY), _at(X), _at(W), _at(pre), _at(slots), _at(offsets),
          _at(dX), _at(dW), _at(db), p, n)

@@ -42,7 +42,7 @@ hipError_t launch_combine_bwd(int dtype, const void *dOut, int64_t ldo, const vo
 // ---- products (fk_linear.hip) ---------------------------------------------------
 struct LinearShape {
     int dtype, ydtype, act, bias_f32;
-    bool grouped;
+    bool grouped, by_slots;             // by_slots: rows of X and dY are taken by a slot list
     int G, share;
     int64_t M, N, K;                    // positions, columns of Y, length of the sum
     int64_t ldx, ldw, ldr, ldy, ldz, lddx;  // row strides

@@ -243,10 +243,10 @@ fk_status check_linear(const fk_linear_shape *h) {
     return FK_OK;
 }
 
-LinearShape shape_of(const fk_linear_shape *h) {
+LinearShape shape_of(const fk_linear_shape *h, bool by_slots) {
     LinearShape s{};
     s.dtype = h->dtype, s.ydtype = h->ydtype, s.act = h->act, s.bias_f32 = h->bias_dtype == FK_F32;
-    s.grouped = h->groups > 0, s.G = h->groups > 0 ? h->groups : 1, s.share = h->share;
+    s.grouped = h->groups > 0, s.by_slots = by_slots, s.G = h->groups > 0 ? h->groups : 1, s.share = h->share;
     s.M = h->M, s.N = h->N, s.K = h->K;
     s.ldx = h->ldx, s.ldw = h->ldw, s.ldr = h->ldr, s.ldy = h->ldy, s.ldz = h->ldpre, s.lddx = h->K;
     return s;
@@ -277,8 +277,9 @@ fk_status check_start(const void *p, int64_t cols, int64_t ld, size_t size, cons
 extern "C" {
 
 size_t fk_linear_workspace_size(const fk_linear_shape *shape, int32_t backward) {
+    // (a list only ever adds to what is needed)
     if (check_linear(shape) != FK_OK) return 0;
-    return plan_linear(shape_of(shape), backward != 0).total;
+    return plan_linear(shape_of(shape, shape->groups > 0 && !(backward & 2)), backward & 1).total;
 }
 
 fk_status fk_linear(const fk_linear_shape *shape, const void *X, const void *W, const void *bias,
@@ -286,7 +287,7 @@ fk_status fk_linear(const fk_linear_shape *shape, const void *X, const void *W, 
                     void *workspace, size_t workspace_bytes, void *stream) {
     g_err[0] = 0;
     FK_CHECK(check_linear(shape));
-    const LinearShape h = shape_of(shape);
+    const LinearShape h = shape_of(shape, slots != nullptr);
     const size_t sz = dtype_size(h.dtype), ysz = dtype_size(h.ydtype), bsz = dtype_size(shape->bias_dtype);
     const int64_t xr = h.M / h.share;
     FK_CHECK(check_matrix(X, xr, h.K, h.ldx, sz, "X"));
@@ -320,7 +321,7 @@ fk_status fk_linear_backward(const fk_linear_shape *shape, const void *dY, const
                              void *dbias, void *workspace, size_t workspace_bytes, void *stream) {
     g_err[0] = 0;
     FK_CHECK(check_linear(shape));
-    const LinearShape h = shape_of(shape);
+    const LinearShape h = shape_of(shape, slots != nullptr);
     const size_t sz = dtype_size(h.dtype), ysz = dtype_size(h.ydtype), bsz = dtype_size(shape->bias_dtype);
     const int64_t xr = h.M / h.share, wr = (int64_t)h.G * h.N;
     FK_CHECK(check_matrix(dY, h.M, h.N, h.ldy, ysz, "dY"));

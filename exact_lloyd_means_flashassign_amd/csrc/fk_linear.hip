@@ -1502,7 +1502,7 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
     p.pad_x = p.tiled && !readable(h.K, h.ldx, h.dtype);
     p.pad_w = p.tiled && !readable(h.K, h.ldw, h.dtype);
     // X by slots past the loads' reach: laid out in position order
-    p.sort_x = p.tiled && h.grouped && !reachable(h.M / h.share, p.pad_x ? kp : h.ldx, h.dtype);
+    p.sort_x = p.tiled && h.by_slots && !reachable(h.M / h.share, p.pad_x ? kp : h.ldx, h.dtype);
     p.pad_x = p.pad_x || p.sort_x;
     const int64_t wrows = groups * h.N;
     if (p.pad_x) p.xpad = take(pad16(p.sort_x ? h.M : h.M / h.share, h.K, h.dtype));
@@ -1516,7 +1516,7 @@ LinearPlan plan_linear(const LinearShape &h, bool backward) {
     }
     // dZ is laid out in position order unless dY serves as it is
     p.make_dz = h.act != FK_ACT_NONE || h.ydtype != h.dtype || !readable(h.N, h.ldy, h.dtype) ||
-                (h.grouped && !reachable(h.M, h.ldy, h.dtype));
+                (h.by_slots && !reachable(h.M, h.ldy, h.dtype));
     if (p.make_dz) p.dz = take(pad16(h.M, h.N, h.dtype));
     p.grad_tiles = h.grouped ? h.M / kGradRows + (h.G < h.M ? h.G : h.M) : cdiv(h.M, kGradRows);
     p.colsum = take((size_t)p.grad_tiles * h.N * 4);

@@ -424,7 +424,8 @@ fk_status fk_route_backward(int32_t dtype, const void *logits, int64_t ldl, int6
  * of bias_dtype (dtype or FK_F32), Y of ydtype (dtype or FK_F32).  X, W and dY
  * whose rows are whole 16-byte chunks (columns and row stride multiples of 8, or
  * of 4 in fp32) are read as they lie and must start on 16 bytes; others are
- * laid out once more in the workspace.  Workspace:
+ * laid out once more in the workspace, and so is an X that a slot list takes
+ * rows from and that is larger than 2 GiB.  Workspace:
  * fk_linear_workspace_size(shape, 0).
  */
 typedef struct {
@@ -435,6 +436,8 @@ typedef struct {
     int64_t M, N, K;                   /* rows of Y, columns of Y, columns of X   */
     int64_t ldx, ldw, ldr, ldy, ldpre; /* row strides of X, W, residual, Y or dY, pre */
 } fk_linear_shape;
+/* backward: 0 for fk_linear, 1 for fk_linear_backward; 2 more (2 or 3) for calls
+ * with slots NULL, which may need less. */
 size_t fk_linear_workspace_size(const fk_linear_shape *shape, int32_t backward);
 fk_status fk_linear(const fk_linear_shape *shape, const void *X, const void *W, const void *bias,
                     const void *residual, const int32_t *slots, const int32_t *offsets, void *Y, void *pre,

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 import exact_lloyd_means_flashassign_amd as fk
-from test_block_cpu import BF16, F32, INVALID, WORKSPACE, P, lib, said, shape  # noqa: F401
+from test_block_cpu import BF16, F32, INVALID, NO_DEVICE, WORKSPACE, P, lib, said, shape  # noqa: F401
 
 
 def linear(lib, h, X=0x10000, W=0x2000000, Y=0x3000000, R=0, pre=0):  # noqa: F811
@@ -69,3 +69,25 @@ def test_where_rows_may_start(lib):  # noqa: F811
     assert linear(lib, shape(M=50, K=127), X=0x10002) == WORKSPACE
     assert linear(lib, shape(M=50, ldx=129), X=0x10002) == WORKSPACE
     assert backward(lib, shape(act=4), pre=0x9000002) == WORKSPACE  # pre may start anywhere
+
+
+def test_workspace_of_rows_in_order(lib):  # noqa: F811
+    """Groups of rows that lie in order need no copy of X or dY, however large;
+    rows by slots do past the reach of 32-bit offsets."""
+    size = lambda h, b: lib.fk_linear_workspace_size(ctypes.byref(h), b)  # noqa: E731
+    M, N, K = 1 << 20, 2048, 2048
+    h = shape(groups=4, M=M, N=N, K=K, ldx=K, ldw=K, ldy=N, ldr=N, ldpre=N)
+    assert size(h, 0) >= M * K * 2 and size(h, 1) >= M * (K + N) * 2
+    assert size(h, 2) < 1 << 20
+    assert size(h, 3) < M // 32 * N * 4 + (64 << 20)  # dbias's column sums, one row for 64
+    for b in (0, 1):
+        few = shape(groups=4, M=4096, N=N, K=K, ldx=K, ldw=K, ldy=N, ldr=N, ldpre=N)
+        assert size(few, b) == size(few, b + 2)
+        plain = shape(M=4096, N=N, K=K, ldx=K, ldw=K, ldy=N, ldr=N, ldpre=N)
+        assert size(plain, b) == size(plain, b + 2)
+    # the calls ask for what they need themselves
+    call = lambda slots: lib.fk_linear(ctypes.byref(h), P(1 << 40), P(2 << 40), None, None, P(slots), P(4 << 40),  # noqa: E731
+                                       P(3 << 40), None, P(5 << 40), 1 << 20, None)
+    assert call(6 << 40) == WORKSPACE
+    if not __import__("torch").cuda.device_count():
+        assert call(0) == NO_DEVICE

@@ -60,3 +60,35 @@ def test_pre_off_16_bytes(gpu_lib):
     for got, want in zip(fk.fk_linear_backward(dY, X, Wt, act="gelu", pre=pre),
                          fk.fk_linear_backward(dY, X, Wt, act="gelu", pre=pre.clone())):
         assert torch.equal(got, want)
+
+
+def test_rows_in_order_past_2_gib(gpu_lib):
+    """Groups of rows that lie in order, X and dY past 2 GiB each: read as they
+    lie, with scratch that holds neither.  Samples against float64."""
+    fk = gpu_lib
+    E, M, N, K, dtype = 3, 1_050_007, 1032, 1032, torch.bfloat16
+    g = torch.Generator(device="cuda:0").manual_seed(1)
+    X, dY = (torch.empty((M, K), dtype=dtype, device="cuda:0").normal_(generator=g) for _ in range(2))
+    assert X.numel() * 2 > 1 << 31
+    Wt = rand(E, N, K, seed=2, scale=K ** -0.5, dtype=dtype)
+    cuts = [0, 300_001, 300_001, M - 11]  # the second group empty, eleven rows past the last
+    offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda:0")
+    scratch = torch.empty(1 << 30, dtype=torch.uint8, device="cuda:0")
+    log("forward")
+    Y, _ = fk.fk_linear(X, Wt, offsets=offsets, workspace=scratch)
+    log("backward")
+    dX, dW, dB = fk.fk_linear_backward(dY, X, Wt, offsets=offsets, workspace=scratch)
+    assert not dW[1].any() and not dB[1].any()
+    for e in (0, 2):
+        lo, hi = cuts[e], cuts[e + 1]
+        at = torch.cat((torch.arange(lo, hi, 40009, device="cuda:0"), torch.arange(hi - 3, hi, device="cuda:0")))
+        x, d, w = X[at].double(), dY[at].double(), Wt[e].double()
+        check(f"Y of {e}", Y[at], (x @ w.t()).cpu(), ((K + 24) * R.W * (x.abs() @ w.abs().t())).cpu(), dtype)
+        check(f"dX of {e}", dX[at], (d @ w).cpu(), ((N + 24) * R.W * (d.abs() @ w.abs())).cpu(), dtype)
+        want, mag = (torch.zeros((8, K), dtype=R.D, device="cuda:0") for _ in range(2))
+        for i in range(lo, hi, 100_000):
+            d, x = dY[i:min(i + 100_000, hi), :8].double(), X[i:min(i + 100_000, hi)].double()
+            want += d.t() @ x
+            mag += d.abs().t() @ x.abs()
+        check(f"dW of {e}", dW[e, :8], want.cpu(), ((hi - lo + 24) * R.W * mag).cpu(), dtype)
+    assert not Y[M - 11:].any() and not dX[M - 11:].any()
