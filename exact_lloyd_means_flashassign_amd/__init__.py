@@ -638,9 +638,12 @@ def fk_layer_norm(X, weight=None, bias=None, eps: float = 1e-5, Y=None):
     return Y, mean, rstd
 
 
-def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = True, dX=None, workspace=None):
-    """Gradients of fk_layer_norm: returns (dX, dweight, dbias); dweight and
-    dbias are None without a weight, dbias also with with_bias=False."""
+def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = True, dX=None, workspace=None,
+                           bias_dtype=None):
+    """Gradients of fk_layer_norm: returns (dX, dweight, dbias).  dweight and
+    dbias are of the weight's type; dbias is None with with_bias=False.  Without
+    a weight dweight is None, and so is dbias unless bias_dtype (the rows' type
+    or fp32) says which it should be."""
     ldx = _rows(X, "X", _FLOATS)
     rows, d = X.shape
     ldd = _rows(dY, "dY", (X.dtype,), (rows, d))
@@ -649,15 +652,19 @@ def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = Tru
     if dX is None:
         dX = torch.empty((rows, d), dtype=X.dtype, device=X.device)
     lddx = _rows(dX, "dX", (X.dtype,), (rows, d))
-    dw = db = None
+    if bias_dtype not in (None, X.dtype, torch.float32):
+        raise ValueError(f"bias_dtype must be {X.dtype} or torch.float32")
+    dw, pdt = None, bias_dtype
     if weight is not None:
         _param(weight, "weight", X.dtype, (d,))
-        dw = torch.empty_like(weight)
-        db = torch.empty_like(weight) if with_bias else None
+        if bias_dtype not in (None, weight.dtype):
+            raise ValueError("weight and bias must be of one type")
+        dw, pdt = torch.empty_like(weight), weight.dtype
+    db = torch.empty(d, dtype=pdt, device=X.device) if with_bias and pdt is not None else None
     dev = _one_device(dY, X, mean, rstd, weight, dX)
     need = load().fk_layer_norm_backward_workspace_size(rows, d) or 256
     p, n, _owner = _scratch(need, dev, workspace)
-    _run(load().fk_layer_norm_backward, dev, DTYPES[X.dtype], DTYPES[X.dtype if weight is None else weight.dtype],
+    _run(load().fk_layer_norm_backward, dev, DTYPES[X.dtype], DTYPES[pdt or X.dtype],
          _at(dY), ldd, _at(X), ldx, rows, d, _at(mean), _at(rstd), _at(weight), _at(dX), lddx, _at(dw), _at(db), p, n)
     return dX, dw, db
 
