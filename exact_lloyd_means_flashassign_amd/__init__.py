@@ -849,17 +849,24 @@ def fk_combine(Y, k: int, gates=None, residual=None, out=None):
 
 
 def fk_combine_backward(dOut, Y, gates):
-    """Gradients of fk_combine: returns (dY [rows k, d], dgates fp32[rows, k])."""
+    """Gradients of fk_combine: returns (dY [rows k, d], dgates fp32[rows, k]),
+    dgates None when gates is (the k is then that of Y's rows)."""
     ldo = _rows(dOut, "dOut", _FLOATS)
     rows, d = dOut.shape
-    _dev(gates, "gates", torch.float32)
-    if gates.dim() != 2 or gates.shape[0] != rows:
-        raise ValueError(f"gates has shape {tuple(gates.shape)}, expected ({rows}, k)")
-    k = gates.shape[1]
-    _dev(Y, "Y", dOut.dtype, (rows * k, d))
+    if gates is None:
+        _dev(Y, "Y", dOut.dtype)
+        if rows == 0 or Y.dim() != 2 or Y.shape[0] % rows != 0 or Y.shape[1] != d:
+            raise ValueError(f"Y has shape {tuple(Y.shape)}, expected (rows k, d) for dOut's {tuple(dOut.shape)}")
+        k = Y.shape[0] // rows
+    else:
+        _dev(gates, "gates", torch.float32)
+        if gates.dim() != 2 or gates.shape[0] != rows:
+            raise ValueError(f"gates has shape {tuple(gates.shape)}, expected ({rows}, k)")
+        k = gates.shape[1]
+        _dev(Y, "Y", dOut.dtype, (rows * k, d))
     dev = _one_device(dOut, Y, gates)
     dY = torch.empty((rows * k, d), dtype=dOut.dtype, device=dOut.device)
-    dgates = torch.empty((rows, k), dtype=torch.float32, device=dOut.device)
+    dgates = None if gates is None else torch.empty((rows, k), dtype=torch.float32, device=dOut.device)
     _run(load().fk_combine_backward, dev, DTYPES[dOut.dtype], _at(dOut), ldo, _at(Y), rows, k, d, _at(gates), _at(dY),
          _at(dgates))
     return dY, dgates

@@ -39,3 +39,16 @@ def test_layer_norm_bias_type_refusals(gpu_lib):
     with pytest.raises(ValueError):
         fk.fk_layer_norm_backward(X, X, mean, rstd, w, bias_dtype=torch.bfloat16)
     assert fk.fk_layer_norm_backward(X, X, mean, rstd, w, bias_dtype=torch.float32)[2].dtype == torch.float32
+
+
+@pytest.mark.parametrize("rows,k,d", [(40, 3, 96), (7, 9, 2052), (3, 2, 9001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_combine_without_gates(gpu_lib, rows, k, d, dtype):
+    """The gradient of a plain sum: every slot gets its row's."""
+    fk = gpu_lib
+    log(f"combine without gates {rows} x {k} x {d} {dtype}")
+    dOut, Y = rand(rows, d, seed=1, dtype=dtype), rand(rows * k, d, seed=2, dtype=dtype)
+    dY, dgates = fk.fk_combine_backward(dOut, Y, None)
+    assert dgates is None and torch.equal(dY, dOut.repeat_interleave(k, 0))
+    with pytest.raises(ValueError):
+        fk.fk_combine_backward(dOut, Y[1:], None)
