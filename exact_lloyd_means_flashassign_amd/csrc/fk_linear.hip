@@ -260,6 +260,17 @@ __device__ __forceinline__ int64_t find_tile(const int32_t *offsets, int G, int6
     return before;
 }
 
+// This workgroup among those of a long grid.  A dimension of a launch takes fewer
+// than 2^32 threads, 2^24 workgroups of 256; where a matrix of one column has
+// more tiles than that, the grid goes on in z.  Workgroups past its end find no
+// tile.
+constexpr int kGridBits = 23;
+__device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.z << kGridBits | blockIdx.x; }
+inline dim3 long_grid(int64_t n, int y = 1) {
+    if (n >> kGridBits == 0) return dim3((unsigned)n, (unsigned)y);
+    return dim3(1u << kGridBits, (unsigned)y, (unsigned)cdiv(n, (int64_t)1 << kGridBits));
+}
+
 // The tile of this workgroup when `total` of them are spread over the 8 XCDs,
 // which take workgroups in turn: each XCD gets a run of consecutive tiles, so
 // that the tiles that share operands share an L2.  -1: none.
@@ -650,10 +661,10 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         // every XCD takes a run of every group's tiles: groups differ in the
         // length of their sums, so runs of whole groups would not be even
         const int64_t per = mtiles * ntiles, run = (per + 7) >> 3;
-        const int64_t i = blockIdx.x >> 3;
+        const int64_t id = workgroup(), i = id >> 3;
         t.g = (int)(i / run);
-        const int64_t in = (blockIdx.x & 7) * run + i % run;
-        if (in >= per) return;
+        const int64_t in = (id & 7) * run + i % run;
+        if (in >= per || t.g >= a.G) return;
         nt = in % ntiles;
         r0 = in / ntiles * BM;
         nrows = a.rows - r0 < BM ? a.rows - r0 : BM;
@@ -665,7 +676,8 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         ka = kb = p1 > pos ? p1 - pos : 0;
     } else if (a.offsets == nullptr) {
         // runs of 8 row tiles by all column tiles
-        const int64_t id = xcd_tile(blockIdx.x, mtiles * ntiles);
+        const int64_t id = xcd_tile(workgroup(), mtiles * ntiles);
+        if (id < 0) return;
         constexpr int GM = 8;
         const int64_t strip = id / (GM * ntiles), in = id % (GM * ntiles);
         const int64_t gm = mtiles - strip * GM < GM ? mtiles - strip * GM : GM;
@@ -677,7 +689,7 @@ __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void 
         const bool rest = !SPLITS || a.splits == 1;
         TileAt none;
         const int64_t tiles = scalar(find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, -1, none));
-        const int64_t id = xcd_tile(blockIdx.x, tiles * ntiles);
+        const int64_t id = xcd_tile(workgroup(), tiles * ntiles);
         if (id < 0) return;
         nt = id % ntiles;
         find_tile(a.offsets, a.G, a.M, BM, a.skip, rest, id / ntiles, t);
@@ -1209,7 +1221,7 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
 // dZ[p] = dY[slot(p)] act'(z[slot(p)]) in position order, rounded to the type
 // that the matrix instructions take (and padded with zeros to whole chunks),
 // and the partial column sums of the unrounded values for db: one row tile of
-// one group and 8 columns a thread.
+// one group (there are `most` of them at most) and 8 columns a thread.
 //
 // Bound by memory.  Workgroups in turn take neighbouring columns of the same
 // rows, so that whole rows are read together: with neighbouring rows' pieces of
@@ -1219,10 +1231,12 @@ __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
 constexpr int kGradRows = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void k_act_grad(LinArgs a, const void *dY, int64_t ldd, int df32, T *dZ, int64_t lddz,
-                                                  float *colsum) {
+                                                  float *colsum, int64_t most) {
     __shared__ float sm[8][256];
     const unsigned cols = (unsigned)((a.N + 255) / 256);
-    const int64_t tile = blockIdx.x / cols, stripe = blockIdx.x % cols;
+    const int64_t id = workgroup();
+    const int64_t tile = id / cols, stripe = id % cols;
+    if (tile >= most) return;
     TileAt t{0, 0, 0};
     if (a.offsets == nullptr) {
         t.p0 = tile * kGradRows;
@@ -1384,7 +1398,7 @@ hipError_t run_product(LinArgs a, int tile, hipStream_t s) {
     }
     if (grid > 0) {
         if (grid > INT32_MAX) return hipErrorInvalidValue;
-        const dim3 gr((unsigned)grid, (unsigned)a.splits);
+        const dim3 gr = long_grid(grid, a.splits);
         if constexpr (sizeof(T) == 2) {
             if (tile == 256) k_product<T, KIND, 256><<<gr, kTileThreads, 0, s>>>(a, mt, nt);
         }
@@ -1611,7 +1625,7 @@ hipError_t linear_bwd(const LinearShape &h, const LinearPlan &p, const LinearBuf
         if (p.grad_tiles > 0) {
             const int64_t grid = p.grad_tiles * cdiv(h.N, 256);
             if (grid > INT32_MAX) return hipErrorInvalidValue;
-            k_act_grad<T><<<(unsigned)grid, 256, 0, s>>>(c, b.dY, h.ldy, h.ydtype == FK_F32, dz, np, cs);
+            k_act_grad<T><<<long_grid(grid), 256, 0, s>>>(c, b.dY, h.ldy, h.ydtype == FK_F32, dz, np, cs, p.grad_tiles);
         }
         if (b.db)
             k_bias_grad<T><<<dim3((unsigned)cdiv(h.N, 16), (unsigned)G), 256, 0, s>>>(c, cs, p.grad_tiles, b.db, h.bias_f32);

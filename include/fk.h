@@ -433,7 +433,7 @@ typedef struct {
     int32_t act;                       /* fk_act                                  */
     int32_t groups;                    /* weight matrices by group, 0: one, plain */
     int32_t share;                     /* consecutive slots that share a row of X */
-    int64_t M, N, K;                   /* rows of Y, columns of Y, columns of X   */
+    int64_t M, N, K;                   /* rows of Y (below 2^31), its columns, columns of X */
     int64_t ldx, ldw, ldr, ldy, ldpre; /* row strides of X, W, residual, Y or dY, pre */
 } fk_linear_shape;
 /* backward: 0 for fk_linear, 1 for fk_linear_backward; 2 more (2 or 3) for calls
