@@ -661,7 +661,7 @@ def fk_layer_norm_backward(dY, X, mean, rstd, weight=None, with_bias: bool = Tru
             raise ValueError("weight and bias must be of one type")
         dw, pdt = torch.empty_like(weight), weight.dtype
     db = torch.empty(d, dtype=pdt, device=X.device) if with_bias and pdt is not None else None
-    dev = _one_device(dY, X, mean, rstd, weight, dX)
+    dev = _one_device(dY, X, mean, rstd, weight, dX, workspace)
     need = load().fk_layer_norm_backward_workspace_size(rows, d) or 256
     p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_layer_norm_backward, dev, DTYPES[X.dtype], DTYPES[pdt or X.dtype],
@@ -688,7 +688,7 @@ def fk_route(logits, k: int, norm="chosen", valid=None, workspace=None):
     T, E = logits.shape
     k = int(k)
     _valid_mask(valid, T)
-    dev = _one_device(logits, valid)
+    dev = _one_device(logits, valid, workspace)
     ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
     gates = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
     counts = torch.empty(E, dtype=torch.int32, device=logits.device)
@@ -783,7 +783,7 @@ def fk_linear(X, W, bias=None, act="none", residual=None, slots=None, offsets=No
     if residual is not None:
         h.ldr = _rows(residual, "residual", (X.dtype,), shape)
     pre = torch.empty(shape, dtype=X.dtype, device=X.device) if with_pre else None
-    dev = _one_device(X, W, bias, residual, slots, offsets, Y)
+    dev = _one_device(X, W, bias, residual, slots, offsets, Y, workspace)
     need = load().fk_linear_workspace_size(ctypes.byref(h), 2 if slots is None else 0) or 256
     p, n, _owner = _scratch(need, dev, workspace)
     _run(load().fk_linear, dev, ctypes.byref(h), _at(X), _at(W), _at(bias), _at(residual), _at(slots), _at(offsets),
@@ -810,7 +810,7 @@ def fk_linear_backward(dY, X, W, act="none", pre=None, slots=None, offsets=None,
     if bias_dtype not in (X.dtype, torch.float32):
         raise ValueError(f"bias_dtype must be {X.dtype} or torch.float32")
     h.bias_dtype = DTYPES[bias_dtype]
-    dev = _one_device(dY, X, W, pre, slots, offsets)
+    dev = _one_device(dY, X, W, pre, slots, offsets, workspace)
     dX = torch.empty((h.M, h.K), dtype=X.dtype, device=X.device) if with_dx else None
     dW = torch.empty(W.shape, dtype=X.dtype, device=X.device) if with_dw else None
     db = torch.empty(W.shape[:-1], dtype=bias_dtype, device=X.device) if with_bias else None

@@ -84,3 +84,33 @@ def test_threads_of_one_stream_have_buffers_of_their_own(card, i):
     t.join()
     assert theirs[0][0] == theirs[1][0] != mine[0]
     assert get(300)[:2] == mine[:2]
+
+
+class OnCard(torch.Tensor):
+    """A host tensor that says it lies on a card (nothing here reaches one)."""
+    card = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.card
+
+
+def on_card(card, *shape, dtype=torch.float32):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(OnCard)
+    t.card = card
+    return t
+
+
+def test_a_workspace_of_another_card_is_refused(monkeypatch):
+    """Every other argument on card 0, the workspace on card 1."""
+    def launched(*a):
+        raise AssertionError("the call went on to its launch")
+    monkeypatch.setattr(fk, "_run", launched)
+    ws = on_card(1, 1 << 20, dtype=torch.uint8)
+    X, W, one = on_card(0, 4, 8), on_card(0, 6, 8), on_card(0, 4)
+    for call in (lambda: fk.fk_layer_norm_backward(X, X, one, one, workspace=ws),
+                 lambda: fk.fk_route(X, 2, workspace=ws),
+                 lambda: fk.fk_linear(X, W, workspace=ws),
+                 lambda: fk.fk_linear_backward(on_card(0, 4, 6), X, W, workspace=ws)):
+        with pytest.raises(ValueError, match="different devices"):
+            call()
