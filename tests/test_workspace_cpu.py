@@ -108,7 +108,7 @@ def test_a_workspace_of_another_card_is_refused(monkeypatch):
     monkeypatch.setattr(fk, "_run", launched)
     ws = on_card(1, 1 << 20, dtype=torch.uint8)
     X, W, one = on_card(0, 4, 8), on_card(0, 6, 8), on_card(0, 4)
-    for call in (lambda: fk.fk_layer_norm_backward(X, X, one, one, workspace=ws),
+    for call in (lambda: fk.fk_layer_norm_backward(X, X, one, one, dX=on_card(0, 4, 8), workspace=ws),
                  lambda: fk.fk_route(X, 2, workspace=ws),
                  lambda: fk.fk_linear(X, W, workspace=ws),
                  lambda: fk.fk_linear_backward(on_card(0, 4, 6), X, W, workspace=ws)):
