@@ -525,6 +525,10 @@ def fk_knn(Q, DB, k: int, metric="l2", idx=None, dist=None, workspace=None, scor
 
 
 # ---- the expert block --------------------------------------------------------
+#
+# Each operator is a forward and a backward call on plain tensors: what a call
+# returns has no autograd history, also where its arguments ask for gradients.
+# examples/expert_block.py joins the pairs into autograd functions.
 
 
 def _named(table, name, what) -> int:
@@ -797,7 +801,9 @@ def fk_linear_backward(dY, X, W, act="none", pre=None, slots=None, offsets=None,
     """Gradients of fk_linear: returns (dX, dW, dbias), None for those not
     asked for.  dX has a row for each slot (with share > 1, fk_combine without
     gates adds the rows that share one of X); dW and dbias have the shapes of W
-    and the bias.  pre: what fk_linear kept (needed unless act is "none")."""
+    and the bias.  pre: what fk_linear kept (needed unless act is "none").
+    dY act'(pre), an fp32 dY too, is rounded to X's type before the products
+    (not for dbias); operands in fp32 keep it whole."""
     h = _linear_problem(X, W, act, slots, offsets, share)
     shape = (h.M, h.N)
     h.ldy = _rows(dY, "dY", (X.dtype, torch.float32), shape)

@@ -623,13 +623,16 @@ struct Epilogue {
 //
 // Measured in bf16 at 16384 x 8192 x 4096: forward 780 to 810 us (1360 to 1410
 // TFLOP/s), dX 815, dW 780 to 795, where the library's product takes 743
-// (1480); with gelu and a residual in the epilogue the
-// forward pass takes 960.  In the loop the matrix units are busy 77 % of the
-// time (the loads' issue costs about 12 %), and a workgroup's first loads and last stores, which nothing overlaps with one
-// workgroup a CU, about 15 us of its 100.  In fp32 tiles of 128 reach 147
-// TFLOP/s (8192 x 8192 x 2048 forward 1876 us, the library 1852), and 60 where
-// a few tiles are left for a second round (5003 x 1001 x 769: 320 tiles on 256
-// CUs, 120 us).
+// (1480); with gelu and a residual in the epilogue the forward pass takes 950 to
+// 1030.  Over the whole kernel the matrix units are busy 60 % of the time there,
+// 65 % in dX and 75 % in dW of 16384 x 4096 x 4096, at the 1.55 to 1.63 GHz that
+// the card then sustains; the rest is the loads' issue between the products and a
+// workgroup's first loads and last stores, which nothing overlaps with one
+// workgroup a CU.  The gradients' tiles of 256 spill 2 and 6 registers, outside
+// the loop.  In fp32 tiles of 128 reach 140 to 147 TFLOP/s (8192 x 8192 x 2048
+// forward 1876 to 1974 us, the library 1852), and 61 to 67 where a few are left
+// for a second round (5003 x 1001 x 769, silu and residual: 320 tiles on 256 CUs,
+// 115 to 126 us, and 10 for laying out rows of 769).
 template <typename T, int KIND, int BS>
 __global__ __launch_bounds__(kTileThreads)
 __attribute__((amdgpu_waves_per_eu(BS == 256 ? 1 : 2, BS == 256 ? 1 : 2))) void k_product(LinArgs a, int64_t mtiles,
@@ -1136,9 +1139,11 @@ __global__ __launch_bounds__(256) void k_join(LinArgs a, int kind) {
 // read.  The waves' sums are added in wave order through LDS.  Groups of more
 // rows are left to the tiled product.
 //
-// bf16, weights from memory: one row by 16384 x 4096 28 us (4.8 TB/s; the
-// tiled product 40), 16 rows 35 us (40); 16 rows by 4096 x 4096 13 us (18).
-// More blocks of rows or 8 waves gained nothing.
+// bf16, weights from memory: one row by 16384 x 4096 26 us (5.2 TB/s; the
+// tiled product 40), 16 rows 34 us (40); 16 rows by 4096 x 4096 13 us (18).
+// More blocks of rows or 8 waves gained nothing.  Rows that are no whole 16-byte
+// chunks are read element by element, each load waited for: one row by 16384 x
+// 4095 125 us.
 template <typename T, int NT, int WV, bool WIDE>
 __global__ __launch_bounds__(WV * 64) void k_product_few(LinArgs a) {
     constexpr int E = 16 / (int)sizeof(T);
@@ -1432,9 +1437,12 @@ hipError_t run_few(const LinArgs &a, hipStream_t s) {
 //
 // Tiles of 256 read half as much a product as those of 128 and run at 1350
 // TFLOP/s where those reach 1100 (bf16, 16384 x 8192 x 4096), if there are
-// enough of them: on 256 CUs, 160 tiles of 256 took 80, 78 and 87 us (forward,
-// dX and dW, 4096 x 2560 x 4096) against 88, 85 and 114 for four times as many
-// of 128; 128 tiles of 256 took 84, 67 and 86 against 70, 75 and 84.  In fp32,
+// enough of them: on 256 CUs, 160 tiles of 256 took 80 us forward and 170 for
+// both gradients (4096 x 2560 x 4096) against 86 and 206 for four times as many
+// of 128; 128 tiles of 256 took 76, 67 and 86 (forward, dX, dW) against 63, 75
+// and 84.  (Of short sums with gelu and a residual, tiles of 128 are ahead at
+// more tiles too, two workgroups of a CU covering each other's epilogues: 160 of
+// 256 by a sum of 512 38 us against 31, 256 of them 44 against 40.)  In fp32,
 // whose matrix instructions take 16 times as long, tiles of 128 are never
 // starved: 8192 x 8192 x 2048 1908, 1899 and 1909 us against 1950, 1926 and
 // 2142, 4096 x 5120 x 1024 365, 298 and 471 against 503, 1197 and 1050.

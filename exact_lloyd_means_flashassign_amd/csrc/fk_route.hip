@@ -22,9 +22,11 @@
 // which leaves 29 bits of its fraction free, with the expert's index in the
 // lowest 10, so that one comparison settles ties too and names the expert.
 // At many rows this arithmetic, not memory, is the forward pass's bound:
-// 262144 rows of 128 experts, k = 8, fp32 take 98 us where their bytes alone
-// would take 30.  The backward pass, which only reads, scales and writes, takes 61 us (4.7
-// TB/s).  16 rows of 64 experts take 6 us, one launch.
+// 262144 rows of 128 experts, k = 8, fp32 take 100 us, the vector units busy for
+// 87 % of them, where their bytes alone would take 30; in bf16 96 us.  The
+// backward pass, which only reads, scales and writes, takes 62 us (4.7 TB/s; bf16
+// 51).  16 rows of 64 experts take 6 us, one launch.  Above 512 experts, 16
+// logits a lane, the forward kernel spills 19 to 29 registers.
 //
 // Selection compares logits as they are (no rounding), the lower index first
 // on ties; a row that is not valid or has nothing above -inf is not live: its
@@ -264,7 +266,9 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     int nlive = 0;
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-    // the next row's logits are under way while this one is worked on
+    // the next row's logits are sent for before this one is worked on: in fp32
+    // they are under way meanwhile (the row's valid flag, if there are any, is
+    // waited for first); 16-bit ones are converted, and so waited for, at once
     float ahead[VPL];
     auto fetch = [&](int64_t r) {
         load_row<T, VPL>(a, r, col, r < a.T && (a.valid == nullptr || a.valid[r] != 0), ahead);

@@ -49,9 +49,10 @@ __device__ __forceinline__ void load_param(const void *p, bool f32, int64_t at, 
 
 // ---- lane exchanges ----
 // Step O of a reduction over aligned groups of lanes, each lane of a group of
-// O holding the same value: v of the neighbouring group of O.  Up to 16 lanes
-// these are data-parallel moves of the vector ALU (quad permutations and
-// mirrors), beyond them the row swaps; none goes through LDS.
+// O holding the same value: v of the neighbouring group of O.  Up to groups of
+// 16 lanes these are data-parallel moves of the vector ALU (quad permutations and
+// mirrors), beyond them permutes through the LDS crossbar, which lanes_reduce
+// spares itself by row swaps.
 template <int O>
 __device__ __forceinline__ uint32_t neighbour(uint32_t v) {
     if constexpr (O == 1) {
