@@ -87,7 +87,8 @@ struct Mma<float> {
 // results too.  Otherwise, for results that are rounded to 16 bits: the
 // hardware's exponential and reciprocal and an approximation of erf, good to
 // 1.5e-7 of |z| where the rounding alone takes 4.9e-4 (fp16) or more of the
-// result, at about a third of the instructions.
+// result.  In fp32, 16384 x 4096 by a sum of 128, the one takes 244 us with gelu
+// and 219 with silu, the other 218 and 198, no activation 184.
 
 // 2^x and 1/x by the hardware's instructions (about an ulp each); an infinite
 // 2^x gives a logistic of 0.
